@@ -570,6 +570,127 @@ int stq1_hessian_error(int format, const void* packed, const float* W, const uin
 int stq1_mix_allocate(const double* err_low, const double* err_high, const double* bytes_low,
                       const double* bytes_high, int64_t n_layers, double budget, uint8_t* pick);
 
+/*
+ * ---- Layers kept at 8 bits, and the unquantised gated block ----
+ * "Precision follows weight sensitivity" (lemmy.durstig.online post 66506):
+ * only the routed experts' projections take the ternary format.  The calls
+ * below serve what stays above it.  The 8-bit integer product is for the
+ * layers every token passes (a shared expert, dense feed-forward layers, the
+ * projections around attention), and stq1_i8_ffn is such a feed-forward layer
+ * next to stq1_moe_ffn.  stq1_glu is the gated block on its bf16 weights,
+ * before quantisation: its output rows are the calibration inputs of the down
+ * projection (stq1_hessian_diag, stq1_hessian_error), and stq1_glu_backward
+ * gives the gradients for recovery training.  The pages describe none of
+ * these; the formats are this library's choice.
+ *
+ * Common to them: row-major contiguous buffers, caller-owned, 16-byte aligned
+ * unless noted (scales: 4 bytes).  Every size is at most 2^30 and every
+ * product of two of a call's sizes at most 2^40, else STQ1_ERR_SHAPE.
+ * Results do not depend on the other rows of a call, and two calls with the
+ * same inputs and sizes give the same bits.  Nothing but the outputs and the
+ * workspace is written.
+ */
+
+/* Element types of stq1_quantize_i8's source and stq1_i8_matmul's result. */
+#define STQ1_TYPE_F32 0
+#define STQ1_TYPE_BF16 1
+
+/*
+ * stq1_quantize_i8 -- signed 8-bit codes of matrix rows: activations (one
+ * scale per token) or weights (one per output channel).  Per row r:
+ * amax = max |src[r, k]|, inv = 127 / amax and scales[r] = amax / 127 (IEEE
+ * fp32 divisions), q[r, k] = the fp32 product src[r, k] * inv rounded to the
+ * nearest integer, ties to even, always in [-127, 127].  src ~= scales[r] * q.
+ * A row with amax < 2^-119 counts as zero: codes and scale 0.  A row holding
+ * an Inf or a NaN gets codes 0 and a scale of Inf or NaN, so that products
+ * with it are NaN and the fault is not hidden.
+ *   src     device, [R, K] bf16 bits or fp32.
+ *   type    STQ1_TYPE_BF16 or STQ1_TYPE_F32: the type of src.
+ *   q       device, [R, K] signed bytes (fully overwritten).
+ *   scales  device, [R] fp32 (fully overwritten).
+ * Requires K % 16 == 0.  Asynchronous on `stream`.
+ * Errors: STQ1_ERR_NULL, STQ1_ERR_ARG (type), STQ1_ERR_SHAPE, STQ1_ERR_ALIGN,
+ * STQ1_ERR_CUDA.
+ */
+int stq1_quantize_i8(const void* src, int type, int64_t R, int64_t K, int8_t* q, float* scales, void* stream);
+
+/*
+ * stq1_i8_matmul -- y[t, n] = (acc * x_scales[t]) * w_scales[n] with
+ * acc = sum_k xq[t, k] wq[n, k], the exact 32-bit integer sum, then rounded to
+ * fp32; both products are rounded to fp32 and, with STQ1_TYPE_BF16, the result
+ * once more to bf16.  The result is bit-exact: every kernel gives these bits.
+ *   xq, x_scales  device, [T, K] codes and [T] fp32 (stq1_quantize_i8).
+ *   wq, w_scales  device, [N, K] codes and [N] fp32.
+ *   y             device, [T, N] fp32 or bf16 bits (fully overwritten).
+ *   type          STQ1_TYPE_F32 or STQ1_TYPE_BF16: the type of y.
+ * Requires K % 16 == 0 and K <= 131056 (the sum then fits for any codes, -128
+ * included).  T and N >= 1.  Asynchronous on `stream`.
+ * Errors: STQ1_ERR_NULL, STQ1_ERR_ARG (type), STQ1_ERR_SHAPE, STQ1_ERR_ALIGN,
+ * STQ1_ERR_CUDA.
+ */
+int stq1_i8_matmul(const int8_t* xq, const float* x_scales, const int8_t* wq, const float* w_scales, void* y, int type,
+                   int64_t T, int64_t N, int64_t K, void* stream);
+
+/*
+ * stq1_i8_ffn_workspace / stq1_i8_ffn -- a gated feed-forward layer at 8 bits:
+ *   (xq, sx) = stq1_quantize_i8(x);  y = stq1_i8_matmul(xq, gate/up) in fp32;
+ *   act = stq1_swiglu(y);  (aq, sa) = stq1_quantize_i8(act);
+ *   out = stq1_i8_matmul(aq, down) in fp32,
+ * with the bits of that chain of calls; y and, for few tokens, the codes are
+ * never stored.
+ *   x              device, [T, H] bf16 bits.
+ *   gateup_q, gateup_scales  device, [N, H] codes (gate rows 0..N/2-1, up rows
+ *                  N/2..N-1) and [N] fp32.
+ *   down_q, down_scales      device, [H, N/2] codes and [H] fp32.
+ *   out            device, [T, H] fp32 (fully overwritten).
+ *   ws, ws_bytes   at least stq1_i8_ffn_workspace(T, N, H) bytes; no zero-fill
+ *                  needed.  Calls sharing it must not overlap.
+ * Requires H % 16 == 0, N % 32 == 0, H and N/2 <= 131056.
+ * Errors: STQ1_ERR_NULL, STQ1_ERR_SHAPE, STQ1_ERR_WORKSPACE, STQ1_ERR_ALIGN,
+ * STQ1_ERR_CUDA.
+ */
+size_t stq1_i8_ffn_workspace(int64_t T, int64_t N, int64_t H);
+int stq1_i8_ffn(const uint16_t* x, const int8_t* gateup_q, const float* gateup_scales, const int8_t* down_q,
+                const float* down_scales, float* out, int64_t T, int64_t N, int64_t H, void* ws, size_t ws_bytes,
+                void* stream);
+
+/*
+ * stq1_glu -- the gated block on bf16 weights: y[t, :] = W x[t, :] (fp32
+ * accumulation), act[t, j] = SiLU(g) * u of the fp32 sums g = y[t, j] and
+ * u = y[t, N/2 + j], rounded once to bf16 as by stq1_swiglu.
+ *   x    device, [T, K] bf16 bits.
+ *   W    device, [N, K] bf16 bits (gate rows 0..N/2-1, up rows N/2..N-1).
+ *   act  device, [T, N/2] bf16 bits (fully overwritten).
+ *   y    device, [T, N] bf16 bits: the sums rounded to bf16, kept for
+ *        stq1_glu_backward; NULL: not stored.
+ * Requires N % 16 == 0 and K % 8 == 0.  Asynchronous on `stream`.
+ * Errors: STQ1_ERR_NULL, STQ1_ERR_SHAPE, STQ1_ERR_ALIGN, STQ1_ERR_CUDA.
+ */
+int stq1_glu(const uint16_t* x, const uint16_t* W, uint16_t* act, uint16_t* y, int64_t T, int64_t N, int64_t K,
+             void* stream);
+
+/*
+ * stq1_glu_backward_workspace / stq1_glu_backward -- gradients of stq1_glu for
+ * a given dact, from the kept y: with s = 1 / (1 + e^-g),
+ *   dG = dact * u * s * (1 + g (1 - s)),  dU = dact * g * s,  dY = [dG | dU],
+ *   dx = dY W  (sum over the N rows),  dW = dY^T x  (sum over the T tokens).
+ * dY is formed in fp32 and rounded to bf16 for the products, which accumulate
+ * in fp32; dx and dW are rounded once to bf16.
+ *   dact  device, [T, N/2] bf16 bits.    y  device, [T, N] bf16 bits.
+ *   x     device, [T, K] bf16 bits (read for dW; may be NULL without it).
+ *   W     device, [N, K] bf16 bits (read for dx; may be NULL without it).
+ *   dx    device, [T, K] bf16 bits (fully overwritten), or NULL: not computed.
+ *   dW    device, [N, K] bf16 bits (fully overwritten), or NULL: not computed.
+ *   ws, ws_bytes   at least stq1_glu_backward_workspace(T, N, K) bytes; holds
+ *         dY ([T, N] bf16) afterwards.  Calls sharing it must not overlap.
+ * Requires N % 16 == 0 and K % 8 == 0.  Asynchronous on `stream`.
+ * Errors: STQ1_ERR_NULL (dx and dW both NULL included), STQ1_ERR_SHAPE,
+ * STQ1_ERR_WORKSPACE, STQ1_ERR_ALIGN, STQ1_ERR_CUDA.
+ */
+size_t stq1_glu_backward_workspace(int64_t T, int64_t N, int64_t K);
+int stq1_glu_backward(const uint16_t* dact, const uint16_t* y, const uint16_t* x, const uint16_t* W, uint16_t* dx,
+                      uint16_t* dW, int64_t T, int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -43,6 +43,8 @@ BLOCK_WEIGHTS = 256
 FMT_STQ1_0 = 0
 FMT_STQ2 = 1
 STQ2_BLOCK_BYTES = 66
+TYPE_F32 = 0
+TYPE_BF16 = 1
 
 # Every symbol include/stq1.h declares: name -> (restype, argtypes)
 _c = ctypes
@@ -97,6 +99,18 @@ SIGNATURES = {
                                    _c.c_void_p]),
     "stq1_mix_allocate": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64,
                                      _c.c_double, _c.c_void_p]),
+    "stq1_quantize_i8": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_void_p,
+                                    _c.c_void_p]),
+    "stq1_i8_matmul": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int,
+                                  _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p]),
+    "stq1_i8_ffn_workspace": (_c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int64]),
+    "stq1_i8_ffn": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                               _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "stq1_glu": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64,
+                            _c.c_void_p]),
+    "stq1_glu_backward_workspace": (_c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int64]),
+    "stq1_glu_backward": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                     _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
 }
 
 
@@ -535,6 +549,157 @@ def ep_combine(rows, inv, t: int, topk: int, out=None):
     rc = _load().stq1_ep_combine(rows.data_ptr(), inv.data_ptr(), out.data_ptr(), t, topk, h, _stream(rows))
     _check("stq1_ep_combine", rc)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Layers kept at 8 bits, and the unquantised gated block
+# ---------------------------------------------------------------------------
+
+
+def _operands(dev, *named):
+    """Checks that each (tensor, dtype, shape, name) is a contiguous CUDA tensor on device index ``dev``
+    with that dtype and shape; a None tensor is skipped."""
+    for t, dtype, shape, name in named:
+        if t is None:
+            continue
+        _require(t, dtype, name)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the other operands on cuda:{dev}")
+
+
+def _matrix(t, dtype, name):
+    _require(t, dtype, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
+    return t.shape
+
+
+def _call(name: str, dev: int, *args):
+    """Calls a library function with device ``dev`` current, on its current stream."""
+    torch = _torch()
+    lib = _lib if _lib is not None else _load()
+    if torch.cuda.current_device() == dev:
+        rc = getattr(lib, name)(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(lib, name)(*args)
+    if rc:
+        _check(name, rc)
+
+
+def quantize_i8(src, out=None, scales=None):
+    """bf16 or fp32 rows [R, K] -> (int8 codes [R, K], fp32 scales [R]): per-token codes of activations
+    or per-channel codes of weights."""
+    torch = _torch()
+    f32 = src.dtype is torch.float32
+    r, k = _matrix(src, torch.float32 if f32 else torch.bfloat16, "src")
+    dev = src.get_device()
+    if out is None:
+        out = torch.empty((r, k), dtype=torch.int8, device=src.device)
+    if scales is None:
+        scales = torch.empty((r,), dtype=torch.float32, device=src.device)
+    _operands(dev, (out, torch.int8, (r, k), "out"), (scales, torch.float32, (r,), "scales"))
+    _call("stq1_quantize_i8", dev, src.data_ptr(), TYPE_F32 if f32 else TYPE_BF16, r, k, out.data_ptr(),
+          scales.data_ptr(), _stream(src))
+    return out, scales
+
+
+def i8_matmul(x_q, x_scales, w_q, w_scales, out=None, dtype=None):
+    """y [T, N] = (x_q w_q^T) * x_scales per token * w_scales per channel, from int8 codes [T, K] and [N, K].
+
+    dtype: torch.float32 (default) or torch.bfloat16; taken from ``out`` when that is given."""
+    torch = _torch()
+    t, k = _matrix(x_q, torch.int8, "x_q")
+    n = _matrix(w_q, torch.int8, "w_q")[0]
+    dev = x_q.get_device()
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"i8_matmul gives torch.float32 or torch.bfloat16, not {dtype}")
+    if out is None:
+        out = torch.empty((t, n), dtype=dtype, device=x_q.device)
+    _operands(dev, (x_scales, torch.float32, (t,), "x_scales"), (w_q, torch.int8, (n, k), "w_q"),
+              (w_scales, torch.float32, (n,), "w_scales"), (out, dtype, (t, n), "out"))
+    _call("stq1_i8_matmul", dev, x_q.data_ptr(), x_scales.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(),
+          out.data_ptr(), TYPE_F32 if dtype is torch.float32 else TYPE_BF16, t, n, k, _stream(x_q))
+    return out
+
+
+def _scratch(ws, nbytes, ref):
+    # a tensor of its own for each call, so that calls on two streams, or captured in two graphs, never share one
+    torch = _torch()
+    if ws is None:
+        return torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=ref.device)
+    _require(ws, torch.uint8, "ws")
+    if ws.get_device() != ref.get_device():
+        raise ValueError("ws must be on the operands' device")
+    return ws
+
+
+def i8_ffn(x, gateup_q, gateup_scales, down_q, down_scales, out=None, ws=None):
+    """Gated feed-forward layer at 8 bits: bf16 x [T, H], int8 gate/up [N, H] and down [H, N/2] -> fp32 [T, H]."""
+    torch = _torch()
+    t, h = _matrix(x, torch.bfloat16, "x")
+    n = _matrix(gateup_q, torch.int8, "gateup_q")[0]
+    dev = x.get_device()
+    if out is None:
+        out = torch.empty((t, h), dtype=torch.float32, device=x.device)
+    _operands(dev, (gateup_q, torch.int8, (n, h), "gateup_q"), (gateup_scales, torch.float32, (n,), "gateup_scales"),
+              (down_q, torch.int8, (h, n // 2), "down_q"), (down_scales, torch.float32, (h,), "down_scales"),
+              (out, torch.float32, (t, h), "out"))
+    ws = _scratch(ws, _load().stq1_i8_ffn_workspace(t, n, h), x)
+    _call("stq1_i8_ffn", dev, x.data_ptr(), gateup_q.data_ptr(), gateup_scales.data_ptr(), down_q.data_ptr(),
+          down_scales.data_ptr(), out.data_ptr(), t, n, h, ws.data_ptr(), ws.numel(), _stream(x))
+    return out
+
+
+def glu(x, w, save: bool = False, out=None, y=None):
+    """act [T, N/2] = SiLU(x Wg^T) * (x Wu^T), bf16, for bf16 x [T, K] and the fused w [N, K] (gate rows, then
+    up rows).  With ``save`` returns (act, y): y [T, N] bf16 is what glu_backward needs."""
+    torch = _torch()
+    t, k = _matrix(x, torch.bfloat16, "x")
+    n = _matrix(w, torch.bfloat16, "w")[0]
+    dev = x.get_device()
+    save = save or y is not None
+    if out is None:
+        out = torch.empty((t, n // 2), dtype=torch.bfloat16, device=x.device)
+    if save and y is None:
+        y = torch.empty((t, n), dtype=torch.bfloat16, device=x.device)
+    _operands(dev, (w, torch.bfloat16, (n, k), "w"), (out, torch.bfloat16, (t, n // 2), "out"),
+              (y, torch.bfloat16, (t, n), "y"))
+    _call("stq1_glu", dev, x.data_ptr(), w.data_ptr(), out.data_ptr(), None if y is None else y.data_ptr(), t, n, k,
+          _stream(x))
+    return (out, y) if save else out
+
+
+def glu_backward(dact, y, x, w, dx=None, dw=None, need_dx: bool = True, need_dw: bool = True, ws=None):
+    """Gradients of glu: (dx [T, K], dw [N, K]) in bf16 from dact [T, N/2], the kept y [T, N], x [T, K] and
+    w [N, K]; None in the place of one that is not needed.  x may be None without dw, w without dx."""
+    torch = _torch()
+    t, n = _matrix(y, torch.bfloat16, "y")
+    if not (need_dx or need_dw):
+        raise ValueError("glu_backward: nothing to compute")
+    if need_dx and w is None or need_dw and x is None:
+        raise ValueError("dx needs w, and dw needs x")
+    k = _matrix(x, torch.bfloat16, "x")[1] if x is not None else _matrix(w, torch.bfloat16, "w")[1]
+    dev = y.get_device()
+    if need_dx and dx is None:
+        dx = torch.empty((t, k), dtype=torch.bfloat16, device=y.device)
+    if need_dw and dw is None:
+        dw = torch.empty((n, k), dtype=torch.bfloat16, device=y.device)
+    if not need_dx:
+        dx = None
+    if not need_dw:
+        dw = None
+    _operands(dev, (dact, torch.bfloat16, (t, n // 2), "dact"), (x, torch.bfloat16, (t, k), "x"),
+              (w, torch.bfloat16, (n, k), "w"), (dx, torch.bfloat16, (t, k), "dx"), (dw, torch.bfloat16, (n, k), "dw"))
+    ws = _scratch(ws, _load().stq1_glu_backward_workspace(t, n, k), y)
+    ptr = lambda v: None if v is None else v.data_ptr()  # noqa: E731
+    _call("stq1_glu_backward", dev, dact.data_ptr(), y.data_ptr(), ptr(x), ptr(w), ptr(dx), ptr(dw), t, n, k,
+          ws.data_ptr(), ws.numel(), _stream(y))
+    return dx, dw
 
 
 PATH_AUTO, PATH_TABLE, PATH_TILES, PATH_MMA = 0, 1, 2, 3

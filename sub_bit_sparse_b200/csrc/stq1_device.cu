@@ -1445,3 +1445,5 @@ extern "C" int stq1_hessian_error(int format, const void* packed, const float* W
     return launch_pdl(hess_score_kernel<0>, static_cast<unsigned>(items), kHsThreads, kHsSmemBytes, s, map, a);
   return launch_pdl(hess_score_kernel<1>, static_cast<unsigned>(items), kHsThreads, kHsSmemBytes, s, map, a);
 }
+
+#include "dense_entry.cuh"
