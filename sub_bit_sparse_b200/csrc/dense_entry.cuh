@@ -2,13 +2,16 @@
 // Included by stq1_device.cu after its launch helpers.
 #pragma once
 
-#include "dense_gemm.cuh"
+#include "dense_gemv.cuh"
+#include "dense_tile.cuh"
+#include "glu_grad.cuh"
 #include "quant_i8.cuh"
 
 namespace stq1 {
 namespace {
 
 constexpr long long kDenseMaxDim = 1LL << 30;
+constexpr int kFfnFusedTokens = 16;
 constexpr long long kI8MaxK = 131056;    // 128 * 128 * K stays below 2^31
 
 bool dense_shape_ok(long long a, long long b, long long c) {
@@ -16,12 +19,121 @@ bool dense_shape_ok(long long a, long long b, long long c) {
          a <= (1LL << 40) / b && a <= (1LL << 40) / c && b <= (1LL << 40) / c;
 }
 
+// 2-D map over a row-major matrix [rows, cols] whose boxes are 128 bytes of a
+// row by box_rows rows, in the 128-byte swizzle; what lies outside reads as zero.
+bool make_operand_map(CUtensorMap* map, const void* base, bool i8, long long rows, long long cols, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const int es = i8 ? 1 : 2;
+  cuuint64_t gdim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t gstride[1] = {static_cast<cuuint64_t>(cols) * es};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(kDnStepBytes / es), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t es1[2] = {1, 1};
+  return fn(map, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), gdim,
+            gstride, box, es1, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+std::atomic<bool> g_dense_configured[kMaxDevices];
+template <int EPI, bool AMN, bool BMN>
+bool dense_config() {
+  return cudaFuncSetAttribute(dense_pair_kernel<EPI, AMN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kPairSmemBytes) == cudaSuccess &&
+         cudaFuncSetAttribute(dense_split_kernel<EPI, AMN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kSplitSmemBytes) == cudaSuccess;
+}
+int ensure_dense_configured() {
+  const int dev = current_device();
+  if (dev < 0) return STQ1_ERR_CUDA;
+  if (g_dense_configured[dev].load(std::memory_order_acquire)) return STQ1_OK;
+  std::lock_guard<std::mutex> lock(g_config_mutex);
+  if (g_dense_configured[dev].load(std::memory_order_relaxed)) return STQ1_OK;
+  if (!(dense_config<kEpiI8F32, false, false>() && dense_config<kEpiI8Bf16, false, false>() &&
+        dense_config<kEpiI8Glu, false, false>() && dense_config<kEpiGlu, false, false>() &&
+        dense_config<kEpiBf16, false, true>() && dense_config<kEpiBf16, true, true>())) {
+    cudaGetLastError();
+    return STQ1_ERR_CUDA;
+  }
+  g_dense_configured[dev].store(true, std::memory_order_release);
+  return STQ1_OK;
+}
+
+// A product for the tile kernels: operand a [M rows] and b, each K-major
+// ([rows, K]) or MN-major ([K, rows]).
+struct DenseProduct {
+  const void *a, *b;
+  long long M, N, K;                 // N: outputs; the gated forms have 2N rows in b
+  const float *sx, *sw;
+  void* out;
+  uint16_t* y;
+};
+
+template <int EPI, bool AMN, bool BMN>
+int launch_tiles(const DenseProduct& d, cudaStream_t s) {
+  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
+  int rc = ensure_dense_configured();
+  if (rc != STQ1_OK) return rc;
+  DenseArgs p{};
+  p.M = d.M;
+  p.N = d.N;
+  p.n_k = static_cast<int>((d.K * (I8 ? 1 : 2) + kDnStepBytes - 1) / kDnStepBytes);
+  p.sx = d.sx;
+  p.sw = d.sw;
+  p.out = d.out;
+  p.y = d.y;
+  const long long rows_b = GLU ? 2 * d.N : d.N;
+  const int sms = sm_count();
+  // pairs: 256 rows x 256 columns of B; singles: 128 x 128
+  const long long pm = (d.M + 255) / 256, pn = (rows_b + 255) / 256;
+  const long long qm = (d.M + 127) / 128, qn = (rows_b + 127) / 128;
+  const bool pair = qm * qn > sms;
+  CUtensorMap ma, mb;
+  const int box_a = AMN ? 64 : 128, box_b = BMN || (GLU && !pair) ? 64 : 128;
+  if (!make_operand_map(&ma, d.a, I8, AMN ? d.K : d.M, AMN ? d.M : d.K, box_a) ||
+      !make_operand_map(&mb, d.b, I8, BMN ? d.K : rows_b, BMN ? rows_b : d.K, box_b))
+    return STQ1_ERR_CUDA;
+  if (pair) {
+    if (pm * pn >= (1LL << 30)) return STQ1_ERR_SHAPE;
+    p.tiles_m = static_cast<int>(pm);
+    p.tiles_n = static_cast<int>(pn);
+    const unsigned grid = 2u * static_cast<unsigned>(std::min<long long>(pm * pn, sms / 2));
+    return launch_pdl(dense_pair_kernel<EPI, AMN, BMN>, grid, kPairThreads, kPairSmemBytes, s, ma, mb, p);
+  }
+  p.tiles_m = static_cast<int>(qm);
+  p.tiles_n = static_cast<int>(qn);
+  int S = 1;
+  while (2 * S <= kSplitMax && 2 * S <= p.n_k && qm * qn * 2 * S <= sms) S *= 2;
+  return launch_pdl_cluster(dense_split_kernel<EPI, AMN, BMN>,
+                            dim3(static_cast<unsigned>(qm * qn), static_cast<unsigned>(S)), kSplitThreads,
+                            kSplitSmemBytes, s, static_cast<unsigned>(S), ma, mb, p);
+}
+
+template <int EPI, bool QX>
+int launch_gemv(const GemvArgs& p, cudaStream_t s) {
+  const long long per = epi_glu(EPI) ? 8 : 16;
+  const unsigned grid = static_cast<unsigned>((p.N + per - 1) / per);
+  if (p.T <= 8) return launch_pdl(dense_gemv_kernel<EPI, QX, 1, 4>, grid, kGvThreads, 0, s, p);
+  if (p.T <= 16) return launch_pdl(dense_gemv_kernel<EPI, QX, 2, 4>, grid, kGvThreads, 0, s, p);
+  return launch_pdl(dense_gemv_kernel<EPI, QX, 4, 2>, grid, kGvThreads, 0, s, p);
+}
+
+// A product of K-major operands: few tokens take the gemv kernel.
 template <int EPI>
-int launch_dense(const DenseArgs& p, cudaStream_t s) {
-  const long long gx = (p.M + kDnTile - 1) / kDnTile;
-  const long long gy = std::min<long long>((p.N + kDnTile - 1) / kDnTile, 65535);
-  return launch_pdl_cluster(dense_gemm_kernel<EPI>, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), 256, 0,
-                            s, 1u, p);
+int launch_product(const DenseProduct& d, cudaStream_t s) {
+  if (d.M <= kGvMaxTokens) {
+    GemvArgs g{};
+    g.w = d.b;
+    g.x = d.a;
+    g.sx = d.sx;
+    g.sw = d.sw;
+    g.out = d.out;
+    g.y = d.y;
+    g.N = d.N;
+    g.K = d.K;
+    g.T = static_cast<int>(d.M);
+    return launch_gemv<EPI, false>(g, s);
+  }
+  return launch_tiles<EPI, false, false>(d, s);
 }
 
 int launch_quant_i8(const void* src, int type, long long R, long long K, int8_t* q, float* scales, cudaStream_t s) {
@@ -30,20 +142,9 @@ int launch_quant_i8(const void* src, int type, long long R, long long K, int8_t*
   return launch_pdl(quant_i8_kernel<false>, static_cast<unsigned>(R), kQi8Threads, 0, s, src, K, q, scales);
 }
 
-DenseArgs i8_args(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, void* out, long long T,
-                  long long N, long long K) {
-  DenseArgs p{};
-  p.a = xq;
-  p.b = wq;
-  p.sam = p.sbn = K;
-  p.sak = p.sbk = 1;
-  p.M = T;
-  p.N = N;
-  p.K = K;
-  p.sx = sx;
-  p.sw = sw;
-  p.out = out;
-  return p;
+DenseProduct i8_product(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, void* out, long long T,
+                        long long N, long long K) {
+  return {xq, wq, T, N, K, sx, sw, out, nullptr};
 }
 
 struct I8FfnPlan {
@@ -90,9 +191,9 @@ extern "C" int stq1_i8_matmul(const int8_t* xq, const float* x_scales, const int
   if (!aligned16(xq) || !aligned16(wq) || !aligned16(y) || (reinterpret_cast<uintptr_t>(x_scales) & 3) ||
       (reinterpret_cast<uintptr_t>(w_scales) & 3))
     return STQ1_ERR_ALIGN;
-  const DenseArgs p = i8_args(xq, x_scales, wq, w_scales, y, T, N, K);
+  const DenseProduct p = i8_product(xq, x_scales, wq, w_scales, y, T, N, K);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return type == STQ1_TYPE_F32 ? launch_dense<kEpiI8F32>(p, s) : launch_dense<kEpiI8Bf16>(p, s);
+  return type == STQ1_TYPE_F32 ? launch_product<kEpiI8F32>(p, s) : launch_product<kEpiI8Bf16>(p, s);
 }
 
 extern "C" int stq1_glu(const uint16_t* x, const uint16_t* W, uint16_t* act, uint16_t* y, int64_t T, int64_t N,
@@ -101,17 +202,7 @@ extern "C" int stq1_glu(const uint16_t* x, const uint16_t* W, uint16_t* act, uin
   if (!x || !W || !act) return STQ1_ERR_NULL;
   if (!glu_shape_ok(T, N, K)) return STQ1_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(W) || !aligned16(act) || !aligned16(y)) return STQ1_ERR_ALIGN;
-  DenseArgs p{};
-  p.a = x;
-  p.b = W;
-  p.sam = p.sbn = K;
-  p.sak = p.sbk = 1;
-  p.M = T;
-  p.N = N / 2;
-  p.K = K;
-  p.out = act;
-  p.y = y;
-  return launch_dense<kEpiGlu>(p, static_cast<cudaStream_t>(stream));
+  return launch_product<kEpiGlu>({x, W, T, N / 2, K, nullptr, nullptr, act, y}, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t stq1_glu_backward_workspace(int64_t T, int64_t N, int64_t K) {
@@ -134,33 +225,12 @@ extern "C" int stq1_glu_backward(const uint16_t* dact, const uint16_t* y, const 
   int rc = launch_pdl(glu_dy_kernel, static_cast<unsigned>(grid), 256, 0, s, dact, y, dy, static_cast<long long>(T),
                       static_cast<long long>(N / 2));
   if (rc != STQ1_OK) return rc;
-  DenseArgs p{};
-  p.a = dy;
   if (dx) {                              // dX[t, k] = sum_n dY[t, n] W[n, k]
-    p.b = W;
-    p.sam = N;
-    p.sak = 1;
-    p.sbn = 1;
-    p.sbk = K;
-    p.M = T;
-    p.N = K;
-    p.K = N;
-    p.out = dx;
-    rc = launch_dense<kEpiBf16>(p, s);
+    rc = launch_tiles<kEpiBf16, false, true>({dy, W, T, K, N, nullptr, nullptr, dx, nullptr}, s);
     if (rc != STQ1_OK) return rc;
   }
-  if (dW) {                              // dW[n, k] = sum_t dY[t, n] x[t, k]
-    p.b = x;
-    p.sam = 1;
-    p.sak = N;
-    p.sbn = 1;
-    p.sbk = K;
-    p.M = N;
-    p.N = K;
-    p.K = T;
-    p.out = dW;
-    rc = launch_dense<kEpiBf16>(p, s);
-  }
+  if (dW)                                // dW[n, k] = sum_t dY[t, n] x[t, k]
+    rc = launch_tiles<kEpiBf16, true, true>({dy, x, N, K, T, nullptr, nullptr, dW, nullptr}, s);
   return rc;
 }
 
@@ -186,11 +256,31 @@ extern "C" int stq1_i8_ffn(const uint16_t* x, const int8_t* gateup_q, const floa
   uint16_t* act = reinterpret_cast<uint16_t*>(wsb + f.act_off);
   int8_t* aq = reinterpret_cast<int8_t*>(wsb + f.aq_off);
   float* sa = reinterpret_cast<float*>(wsb + f.sa_off);
+  if (T <= kFfnFusedTokens) {
+    // codes made inside the products: two launches
+    GemvArgs g{};
+    g.w = gateup_q;
+    g.x = x;
+    g.sw = gateup_scales;
+    g.out = act;
+    g.N = N / 2;
+    g.K = H;
+    g.T = static_cast<int>(T);
+    int rc = launch_gemv<kEpiI8Glu, true>(g, s);
+    if (rc != STQ1_OK) return rc;
+    g.w = down_q;
+    g.x = act;
+    g.sw = down_scales;
+    g.out = out;
+    g.N = H;
+    g.K = N / 2;
+    return launch_gemv<kEpiI8F32, true>(g, s);
+  }
   int rc = launch_quant_i8(x, STQ1_TYPE_BF16, T, H, xq, sx, s);
   if (rc != STQ1_OK) return rc;
-  rc = launch_dense<kEpiI8Glu>(i8_args(xq, sx, gateup_q, gateup_scales, act, T, N / 2, H), s);
+  rc = launch_product<kEpiI8Glu>(i8_product(xq, sx, gateup_q, gateup_scales, act, T, N / 2, H), s);
   if (rc != STQ1_OK) return rc;
   rc = launch_quant_i8(act, STQ1_TYPE_BF16, T, N / 2, aq, sa, s);
   if (rc != STQ1_OK) return rc;
-  return launch_dense<kEpiI8F32>(i8_args(aq, sa, down_q, down_scales, out, T, H, N / 2), s);
+  return launch_product<kEpiI8F32>(i8_product(aq, sa, down_q, down_scales, out, T, H, N / 2), s);
 }

@@ -1,0 +1,616 @@
+// Tensor-core products of the 8-bit integer and bf16 gated layers (sm_100a,
+// tcgen05): C[m, n] = sum_k A(m, k) B(n, k), both operands from shared memory,
+// fp32 (bf16 operands) or 32-bit integer (8-bit operands) sums in TMEM, and
+// the layer's arithmetic on each finished sum before it is stored.
+//
+// Operands are K-major (rows of k, as x [T, K] and W [N, K] lie in the forward
+// products) or MN-major (the contraction runs over the rows of the matrix, as
+// in dX = dY W for W and in dW = dY^T x for both), so no transposed copy is
+// ever made: the tensor copies bring 128-byte pieces of rows in both cases and
+// only the descriptors of the MMAs differ.
+#pragma once
+
+#include "dense_math.cuh"
+#include "tc_gemm.cuh"
+
+namespace stq1 {
+
+// What becomes of a finished sum.
+enum DenseEpi {
+  kEpiI8F32,      // int8: fp32 out[m, n]
+  kEpiI8Bf16,     // int8: bf16 out[m, n]
+  kEpiI8Glu,      // int8: bf16 act[m, n] of gate channel n and up channel N + n
+  kEpiGlu,        // bf16: the same, and optionally the sums as bf16 y [m, 2N]
+  kEpiBf16,       // bf16: bf16 out[m, n]
+};
+__host__ __device__ constexpr bool epi_i8(int e) { return e == kEpiI8F32 || e == kEpiI8Bf16 || e == kEpiI8Glu; }
+__host__ __device__ constexpr bool epi_glu(int e) { return e == kEpiI8Glu || e == kEpiGlu; }
+
+struct DenseArgs {
+  long long M, N;                    // outputs; for the gated forms N is half of B's rows
+  int n_k;                           // 128-byte steps of K
+  int tiles_m, tiles_n;
+  const float *sx, *sw;              // int8: scales of A's rows and of B's rows
+  void* out;                         // [M, N]
+  uint16_t* y;                       // kEpiGlu: [M, 2N] or NULL
+};
+
+constexpr int kDnStepBytes = 128;    // bytes of K per step and row: one swizzle atom
+constexpr int kDnRows = 128;         // rows of A and rows of B per CTA and step
+constexpr int kDnOperandBytes = kDnRows * kDnStepBytes;
+constexpr int kDnStageBytes = 2 * kDnOperandBytes;
+
+// ---- PTX wrappers (pairs of CTAs) ----
+template <int CG>
+__device__ __forceinline__ void dn_tmem_alloc(uint32_t dst_smem, uint32_t cols) {
+  if constexpr (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst_smem, cols);
+    tmem_relinquish();
+  }
+}
+template <int CG>
+__device__ __forceinline__ void dn_tmem_dealloc(uint32_t taddr, uint32_t cols) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+  else
+    tmem_dealloc(taddr, cols);
+}
+// Arrives on the barrier at this offset in both CTAs of the pair once the
+// MMAs issued so far are done.
+__device__ __forceinline__ void dn_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ uint32_t dn_mapa(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void dn_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// As mbar_wait_bounded, for arrivals from the other CTA of the cluster.
+__device__ __forceinline__ bool dn_wait_cluster(uint32_t bar, uint32_t parity) {
+  for (uint32_t i = 0; i < (1u << 14); ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(kWaitHintNs)
+        : "memory");
+    if (done) return true;
+  }
+  flag_error(STQ1_DEV_WAIT_LIMIT);
+  return false;
+}
+// 2-D tensor copy into this CTA; in a pair the bytes are counted on the
+// leader's barrier (bar is then a shared::cluster address).
+template <int CG>
+__device__ __forceinline__ void dn_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    tma_load_2d(dst, map, x, y, bar);
+}
+template <bool I8, int CG>
+__device__ __forceinline__ void dn_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+#define STQ1_DN_MMA(CGS, KIND)                                                                       \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                      \
+               "tcgen05.mma.cta_group::" CGS ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d),    \
+               "l"(a), "l"(b), "r"(idesc), "r"(accumulate)                                            \
+               : "memory")
+  if constexpr (I8 && CG == 2) STQ1_DN_MMA("2", "i8");
+  else if constexpr (I8) STQ1_DN_MMA("1", "i8");
+  else if constexpr (CG == 2) STQ1_DN_MMA("2", "f16");
+  else STQ1_DN_MMA("1", "f16");
+#undef STQ1_DN_MMA
+}
+
+// Shared-memory descriptors, 128-byte swizzle.  K-major: rows of 128 bytes,
+// groups of 8 rows 1024 bytes apart; an MMA (32 bytes of K) advances the
+// start by 32 bytes.  MN-major: blocks of 64 bf16 values along MN (8 KB: one
+// 128-byte row per k, 64 of them), groups of 8 k 1024 bytes apart; an MMA (16
+// values of k) advances the start by 2048 bytes.
+template <bool MN>
+__device__ __forceinline__ uint64_t dn_desc(uint32_t addr) {
+  if constexpr (MN)
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(8192 >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+  else
+    return smem_desc_sw128(addr);
+}
+template <bool MN>
+constexpr uint32_t dn_advance() { return MN ? 2048u >> 4 : 32u >> 4; }
+
+// Instruction descriptor: D fp32 or 32-bit integer (bits 4-5), A and B bf16 or
+// signed 8-bit (bits 7-9, 10-12: 1 in both kinds), MN-major A and B (bits 15,
+// 16), N >> 3 at bit 17, M >> 4 at bit 24.
+template <bool I8, bool AMN, bool BMN>
+constexpr uint32_t dn_idesc(int m, int n) {
+  return (I8 ? 2u << 4 : 1u << 4) | (1u << 7) | (1u << 10) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// One step of an operand into shared memory: 128 rows (K-major) or 128
+// columns (MN-major, two boxes of 64) of 128 bytes of K.
+template <bool I8, bool MN, int CG>
+__device__ __forceinline__ void dn_load_operand(uint32_t dst, const CUtensorMap* map, int step, int row, uint32_t bar) {
+  constexpr int kStep = I8 ? 128 : 64;      // values of K per step
+  if constexpr (MN) {
+    dn_load<CG>(dst, map, row, step * kStep, bar);
+    dn_load<CG>(dst + kDnOperandBytes / 2, map, row + 64, step * kStep, bar);
+  } else {
+    dn_load<CG>(dst, map, step * kStep, row, bar);
+  }
+}
+
+template <bool I8>
+__device__ __forceinline__ float dn_sum(uint32_t v, float sx, float sw) {
+  if constexpr (I8) return i8_value(static_cast<int>(v), sx, sw);
+  else return __uint_as_float(v);
+}
+
+// Position of a tile: groups of kDnGroup row tiles, column by column, so that
+// the tiles in flight share rows of A and of B in L2.
+constexpr int kDnGroup = 8;
+__device__ __forceinline__ void dn_tile_pos(const DenseArgs& p, int tile, int& tm, int& tn) {
+  const int per = kDnGroup * p.tiles_n;
+  const int g = tile / per, in = tile - g * per;
+  const int rows = min(kDnGroup, p.tiles_m - g * kDnGroup);
+  tn = in / rows;
+  tm = g * kDnGroup + in - tn * rows;
+}
+
+// ---------------------------------------------------------------------------
+// Large products: pairs of CTAs on 256 x 256 tiles.
+// ---------------------------------------------------------------------------
+
+constexpr int kPairStages = 6;
+constexpr int kPairThreads = 320;                   // warps 0-7 epilogue, 8 producer, 9 MMA
+constexpr int kPairOffStage = kPairStages * kDnStageBytes;
+constexpr int kPairOffBar = kPairOffStage + 8 * 4096;
+constexpr int kPairSmemBytes = 1024 + kPairOffBar + 256;
+static_assert(kPairSmemBytes <= 232448, "shared memory per CTA is at most 227 KB");
+
+// One warp's 32 x 32 words (row = lane) to global memory through 4 KB of
+// shared memory: 16-byte pieces at piece ^ (row & 7), so that neither the
+// row-wise stores nor the reads of whole rows meet on a bank; then eight lanes
+// store 128 bytes of one row.  ES: bytes of an element; a word holds 4 / ES.
+template <int ES>
+__device__ __forceinline__ void dn_store_block(const uint32_t (&w)[32], uint32_t buf, void* out, long long row0,
+                                               long long rows, long long ld, long long col0, long long cols, bool vec) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPer = 4 / ES;                      // elements per word
+  __syncwarp();                                     // the previous block's reads are done
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(buf + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(w[4 * c]),
+                 "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                 : "memory");
+  __syncwarp();
+  char* base = static_cast<char*>(out);
+  const int piece = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    if (row0 + r >= rows) continue;
+    const uint4 v = lds_v4(buf + r * 128 + ((piece ^ (r & 7)) << 4));
+    const long long c = col0 + piece * 4 * kPer;
+    char* dst = base + ((row0 + r) * ld + c) * ES;
+    if (vec) {
+      if (c < cols) *reinterpret_cast<uint4*>(dst) = v;       // cols is then a multiple of 16 / ES
+    } else {
+      const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4 * kPer; ++j)
+        if (c + j < cols) {
+          if constexpr (ES == 4) reinterpret_cast<uint32_t*>(dst)[j] = e[j];
+          else reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>(e[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+  }
+}
+
+template <int EPI, bool AMN, bool BMN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                  const DenseArgs p) {
+  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
+  static_assert(!(I8 && (AMN || BMN)), "8-bit operands are K-major");
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const uint32_t sraw = smem_u32(smem_raw);
+  const uint32_t sbase = (sraw + 1023u) & ~1023u;
+  const uint32_t bar = sbase + kPairOffBar;
+  const uint32_t bar_full = bar, bar_empty = bar + 64, bar_acc_full = bar + 128, bar_acc_empty = bar + 144,
+                 bar_drain = bar + 160, s_tmem = bar + 176;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(bar_full + 8 * i, 1);
+      mbar_init(bar_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_acc_full + 8 * i, 1);
+      mbar_init(bar_acc_empty + 8 * i, 16);          // the epilogue warps of both CTAs
+    }
+    mbar_init(bar_drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) dn_tmem_alloc<2>(s_tmem, 512);
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(s_tmem));
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int n_tiles = p.tiles_m * p.tiles_n;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (warp == 8) {
+    // ---- producer: this CTA's 128 rows of A and 128 rows of B per step ----
+    // A wait that runs out ends the role; it started after the last copy was
+    // issued, so no copy is in flight any more by then.
+    if (lane == 0) {
+      const uint32_t full0 = dn_mapa(bar_full, 0);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = first; tile < n_tiles && ok; tile += step) {
+        int tm, tn;
+        dn_tile_pos(p, tile, tm, tn);
+        const int row_a = tm * 256 + static_cast<int>(rank) * kDnRows;
+        // gated: the leader loads the gate rows, its peer the up rows of the same outputs
+        const int row_b = GLU ? static_cast<int>(rank * p.N) + tn * kDnRows : tn * 256 + static_cast<int>(rank) * kDnRows;
+        for (int k = 0; k < p.n_k; ++k, ++it) {
+          const uint32_t s = it % kPairStages, use = it / kPairStages;
+          if (!mbar_wait_bounded(bar_empty + 8 * s, (use & 1) ^ 1)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, 2 * kDnStageBytes);
+          const uint32_t dst = sbase + s * kDnStageBytes;
+          dn_load_operand<I8, AMN, 2>(dst, &map_a, k, row_a, full0 + 8 * s);
+          dn_load_operand<I8, BMN, 2>(dst + kDnOperandBytes, &map_b, k, row_b, full0 + 8 * s);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ---- MMA issuer (leader only): both CTAs' operands, both CTAs' TMEM ----
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = dn_idesc<I8, AMN, BMN>(256, 256);
+      uint32_t it = 0, t = 0;
+      bool ok = true;
+      for (int tile = first; tile < n_tiles && ok; tile += step, ++t) {
+        const uint32_t buf = t & 1, use = t >> 1;
+        if (!dn_wait_cluster(bar_acc_empty + 8 * buf, (use & 1) ^ 1)) break;
+        tc_fence_after();
+        for (int k = 0; k < p.n_k; ++k, ++it) {
+          const uint32_t s = it % kPairStages, ph = (it / kPairStages) & 1;
+          if (!dn_wait_cluster(bar_full + 8 * s, ph)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t da = dn_desc<AMN>(sbase + s * kDnStageBytes);
+          const uint64_t db = dn_desc<BMN>(sbase + s * kDnStageBytes + kDnOperandBytes);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            dn_mma<I8, 2>(tmem + 256 * buf, da + j * dn_advance<AMN>(), db + j * dn_advance<BMN>(), idesc, (k | j) != 0);
+          dn_commit_pair(bar_empty + 8 * s);
+        }
+        dn_commit_pair(bar_acc_full + 8 * buf);
+      }
+      if (!ok) {
+        // every MMA issued must be done before TMEM is freed (bounded)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar_drain)
+                     : "memory");
+        mbar_wait_bounded(bar_drain, 0);
+      }
+    }
+  } else {
+    // ---- epilogue: warp w reads TMEM lanes 32 (w & 3).. and half of the columns ----
+    const int quad = warp & 3, half = warp >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+    const uint32_t buf_s = sbase + kPairOffStage + warp * 4096;
+    const uint32_t acc_empty0 = dn_mapa(bar_acc_empty, 0);
+    constexpr int ES = EPI == kEpiI8F32 ? 4 : 2;
+    const bool vec = p.N % (16 / ES) == 0;
+    uint32_t t = 0;
+    for (int tile = first; tile < n_tiles; tile += step, ++t) {
+      const uint32_t buf = t & 1, use = t >> 1;
+      int tm, tn;
+      dn_tile_pos(p, tile, tm, tn);
+      const long long row0 = tm * 256LL + rank * kDnRows + 32 * quad;
+      const float sx = I8 && row0 + lane < p.M ? p.sx[row0 + lane] : 0.f;
+      if (!mbar_wait_bounded(bar_acc_full + 8 * buf, use & 1)) break;
+      tc_fence_after();
+      const uint32_t acc = lanes + 256 * buf;
+      // scale of column col0 + lane of B (0 past the end)
+      auto col_scale = [&](long long first_row, long long col0) {
+        return I8 && col0 + lane < p.N ? p.sw[first_row + col0 + lane] : 0.f;
+      };
+      if constexpr (GLU) {
+        // act columns [64 half, 64 half + 64) of the tile: gate sums at those columns, up sums 128 further
+        const long long col0 = tn * 128LL + 64 * half;
+        uint32_t act[32], kg[32], ku[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t g[16], u[16];
+          STQ1_TMEM_LD16(acc + 64 * half + 16 * c, g);
+          STQ1_TMEM_LD16(acc + 128 + 64 * half + 16 * c, u);
+          float swg = 0.f, swu = 0.f;
+          if constexpr (I8) {
+            swg = col_scale(0, col0 + 16 * c);
+            swu = col_scale(p.N, col0 + 16 * c);
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float gv[2], uv[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              gv[h] = dn_sum<I8>(g[i + h], sx, I8 ? __shfl_sync(0xffffffffu, swg, i + h) : 0.f);
+              uv[h] = dn_sum<I8>(u[i + h], sx, I8 ? __shfl_sync(0xffffffffu, swu, i + h) : 0.f);
+            }
+            act[8 * c + i / 2] = swiglu_bf16(gv[0], uv[0]) | (swiglu_bf16(gv[1], uv[1]) << 16);
+            if constexpr (EPI == kEpiGlu) {
+              kg[8 * c + i / 2] = bf16_bits_rn(gv[0]) | (bf16_bits_rn(gv[1]) << 16);
+              ku[8 * c + i / 2] = bf16_bits_rn(uv[0]) | (bf16_bits_rn(uv[1]) << 16);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dn_arrive_remote(acc_empty0 + 8 * buf);
+        dn_store_block<2>(act, buf_s, p.out, row0, p.M, p.N, col0, p.N, vec);
+        if constexpr (EPI == kEpiGlu)
+          if (p.y) {
+            dn_store_block<2>(kg, buf_s, p.y, row0, p.M, 2 * p.N, col0, p.N, vec);
+            dn_store_block<2>(ku, buf_s, p.y + p.N, row0, p.M, 2 * p.N, col0, p.N, vec);
+          }
+      } else {
+        constexpr int kCols = 128 / ES;              // columns of one 128-byte block of a row
+#pragma unroll 1
+        for (int c = 0; c < 128 / kCols; ++c) {
+          const int tc = 128 * half + kCols * c;
+          const long long col0 = tn * 256LL + tc;
+          uint32_t w[32];
+#pragma unroll
+          for (int q = 0; q < kCols / 32; ++q) {
+            uint32_t v[32];
+            STQ1_TMEM_LD32(acc + tc + 32 * q, v);
+            const float sw = col_scale(0, col0 + 32 * q);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float f[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) f[h] = dn_sum<I8>(v[i + h], sx, I8 ? __shfl_sync(0xffffffffu, sw, i + h) : 0.f);
+              if constexpr (ES == 4) {
+                w[i] = __float_as_uint(f[0]);
+                w[i + 1] = __float_as_uint(f[1]);
+              } else {
+                w[16 * q + i / 2] = bf16_bits_rn(f[0]) | (bf16_bits_rn(f[1]) << 16);
+              }
+            }
+          }
+          if (c == 128 / kCols - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) dn_arrive_remote(acc_empty0 + 8 * buf);
+          }
+          dn_store_block<ES>(w, buf_s, p.out, row0, p.M, p.N, col0, p.N, vec);
+        }
+      }
+    }
+  }
+
+  // all roles of both CTAs meet here (every wait above is bounded): the
+  // barriers and shared memory a peer uses stay alive until it is done
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 9) {
+    tc_fence_after();
+    dn_tmem_dealloc<2>(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Products with few tiles: one CTA per 128 x 128 tile and piece of K.
+// ---------------------------------------------------------------------------
+
+constexpr int kSplitStages = 6;
+constexpr int kSplitThreads = 192;                  // warps 0-3 epilogue, 4 producer, 5 MMA
+constexpr int kSplitMax = 8;                        // pieces of K: the CTAs of one cluster
+constexpr int kSplitPitch = 132;                    // words per row of a finished piece
+constexpr int kSplitOffBar = kSplitStages * kDnStageBytes;
+constexpr int kSplitSmemBytes = 1024 + kSplitOffBar + 256;
+static_assert(kDnRows * kSplitPitch * 4 <= kSplitOffBar, "a finished piece takes the place of the stages");
+
+// Each CTA of a cluster sums its piece of K (steps [k0, k1)) in TMEM and lays
+// the 128 x 128 sums into its shared memory; each then adds up its share of
+// the rows over all pieces, in the order of the pieces, and stores them: the
+// result does not depend on which CTA comes first.
+template <int EPI, bool AMN, bool BMN>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const DenseArgs p) {
+  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const uint32_t sraw = smem_u32(smem_raw);
+  const uint32_t sbase = (sraw + 1023u) & ~1023u;
+  const uint32_t bar = sbase + kSplitOffBar;
+  const uint32_t bar_full = bar, bar_empty = bar + 64, bar_acc = bar + 128, s_tmem = bar + 144;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = gridDim.y, piece = blockIdx.y;       // the cluster runs along y
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSplitStages; ++i) {
+      mbar_init(bar_full + 8 * i, 1);
+      mbar_init(bar_empty + 8 * i, 1);
+    }
+    mbar_init(bar_acc, 1);
+    fence_mbar_init();
+  }
+  if (warp == 5) dn_tmem_alloc<1>(s_tmem, 128);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(s_tmem));
+  griddep_wait();
+  griddep_launch_dependents();
+
+  int tm, tn;
+  dn_tile_pos(p, blockIdx.x, tm, tn);
+  const int k0 = static_cast<int>(static_cast<long long>(p.n_k) * piece / S);
+  const int k1 = static_cast<int>(static_cast<long long>(p.n_k) * (piece + 1) / S);
+  constexpr int kOutCols = GLU ? 64 : 128;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      for (int k = k0; k < k1; ++k) {
+        const uint32_t it = k - k0, s = it % kSplitStages, use = it / kSplitStages;
+        if (!mbar_wait_bounded(bar_empty + 8 * s, (use & 1) ^ 1)) break;
+        mbar_arrive_expect_tx(bar_full + 8 * s, kDnStageBytes);
+        const uint32_t dst = sbase + s * kDnStageBytes, b = bar_full + 8 * s;
+        dn_load_operand<I8, AMN, 1>(dst, &map_a, k, tm * kDnRows, b);
+        if constexpr (GLU) {
+          // 64 gate rows and the 64 up rows of the same outputs (boxes of 64 rows)
+          const int step = k * (I8 ? 128 : 64);
+          dn_load<1>(dst + kDnOperandBytes, &map_b, step, tn * 64, b);
+          dn_load<1>(dst + kDnOperandBytes + kDnOperandBytes / 2, &map_b, step, static_cast<int>(p.N) + tn * 64, b);
+        } else {
+          dn_load_operand<I8, BMN, 1>(dst + kDnOperandBytes, &map_b, k, tn * kDnRows, b);
+        }
+      }
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = dn_idesc<I8, AMN, BMN>(128, 128);
+      for (int k = k0; k < k1; ++k) {
+        const uint32_t it = k - k0, s = it % kSplitStages, ph = (it / kSplitStages) & 1;
+        if (!mbar_wait_bounded(bar_full + 8 * s, ph)) break;
+        tc_fence_after();
+        const uint64_t da = dn_desc<AMN>(sbase + s * kDnStageBytes);
+        const uint64_t db = dn_desc<BMN>(sbase + s * kDnStageBytes + kDnOperandBytes);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          dn_mma<I8, 1>(tmem, da + j * dn_advance<AMN>(), db + j * dn_advance<BMN>(), idesc, (it | j) != 0);
+        tc_commit(bar_empty + 8 * s);
+      }
+      tc_commit(bar_acc);                            // all MMAs so far, in the error case too
+    }
+  } else {
+    // the sums to shared memory (the stages are free once the last MMA is done)
+    mbar_wait_bounded(bar_acc, 0);
+    tc_fence_after();
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const uint32_t row = sbase + (32 * warp + lane) * (kSplitPitch * 4);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t v[32];
+      STQ1_TMEM_LD32(lanes + 32 * c, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + 128 * c + 4 * i), "r"(v[i]), "r"(v[i + 1]),
+                     "r"(v[i + 2]), "r"(v[i + 3])
+                     : "memory");
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();                                // every piece lies in shared memory
+  if (warp == 5) {
+    tc_fence_after();
+    dn_tmem_dealloc<1>(tmem, 128);
+  }
+
+  // this CTA's rows: piece, piece + S, ... ; a warp takes a row, a lane four sums (or two gate/up pairs)
+  const long long m0 = static_cast<long long>(tm) * kDnRows;
+  const long long n0 = static_cast<long long>(tn) * kOutCols;
+  const int rows = static_cast<int>(min(static_cast<long long>(kDnRows), p.M - m0));
+  const int c0 = GLU ? 2 * lane : 4 * lane;          // first output column of this lane
+  float swa[4] = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (I8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long col = n0 + c0 + (GLU ? (i & 1) : i);
+      if (col < p.N) swa[i] = p.sw[(GLU && i >= 2 ? p.N : 0) + col];
+    }
+  }
+  for (int r = piece + S * warp; r < rows; r += S * (kSplitThreads / 32)) {
+    const uint32_t at = sbase + r * (kSplitPitch * 4);
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    for (int q = 0; q < S; ++q) {
+      const uint32_t src = dn_mapa(at, q);
+      uint32_t w[4];
+      if constexpr (GLU) {
+        asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src + 8 * lane) : "memory");
+        asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "r"(src + 256 + 8 * lane) : "memory");
+      } else {
+        asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(src + 16 * lane)
+                     : "memory");
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (I8) v[i] += w[i];
+        else v[i] = q == 0 ? w[i] : __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+      }
+    }
+    const long long m = m0 + r;
+    const float sx = I8 ? p.sx[m] : 0.f;
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = dn_sum<I8>(v[i], sx, swa[i]);
+    const long long col = n0 + c0;
+    if constexpr (GLU) {
+      // N is a multiple of 8 here and c0 even, so both columns exist or neither does
+      if (col < p.N) {
+        const uint32_t a = swiglu_bf16(f[0], f[2]) | (swiglu_bf16(f[1], f[3]) << 16);
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + m * p.N + col) = a;
+        if constexpr (EPI == kEpiGlu)
+          if (p.y) {
+            uint16_t* yr = p.y + m * 2 * p.N + col;
+            *reinterpret_cast<uint32_t*>(yr) = bf16_bits_rn(f[0]) | (bf16_bits_rn(f[1]) << 16);
+            *reinterpret_cast<uint32_t*>(yr + p.N) = bf16_bits_rn(f[2]) | (bf16_bits_rn(f[3]) << 16);
+          }
+      }
+    } else if constexpr (EPI == kEpiI8F32) {
+      float* dst = static_cast<float*>(p.out) + m * p.N + col;
+      if (p.N % 4 == 0) {
+        if (col < p.N) *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (col + i < p.N) dst[i] = f[i];
+      }
+    } else {
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + m * p.N + col;
+      const uint32_t lo = bf16_bits_rn(f[0]) | (bf16_bits_rn(f[1]) << 16);
+      const uint32_t hi = bf16_bits_rn(f[2]) | (bf16_bits_rn(f[3]) << 16);
+      if (p.N % 4 == 0) {
+        if (col < p.N) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (col + i < p.N) dst[i] = static_cast<uint16_t>((i < 2 ? lo : hi) >> (16 * (i & 1)));
+      }
+    }
+  }
+  cluster_sync_all();                                // a peer may still read this CTA's piece
+}
+
+}  // namespace stq1
