@@ -556,53 +556,69 @@ def ep_combine(rows, inv, t: int, topk: int, out=None):
 # ---------------------------------------------------------------------------
 
 
-def _operands(dev, *named):
-    """Checks that each (tensor, dtype, shape, name) is a contiguous CUDA tensor on device index ``dev``
-    with that dtype and shape; a None tensor is skipped."""
-    for t, dtype, shape, name in named:
-        if t is None:
-            continue
-        _require(t, dtype, name)
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the other operands on cuda:{dev}")
-
-
 def _matrix(t, dtype, name):
+    """The shape of a contiguous CUDA matrix of that dtype."""
     _require(t, dtype, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
     return t.shape
 
 
-def _call(name: str, dev: int, *args):
-    """Calls a library function with device ``dev`` current, on its current stream."""
+def _operand(t, dtype, shape, dev, name):
+    """Checks a contiguous CUDA tensor of that dtype and shape on device index ``dev``; returns its address."""
+    if getattr(t, "dtype", None) is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _require(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the other operands on cuda:{dev}")
+
+
+_get_device = None
+
+
+def _call(name: str, dev: int, fn, *args):
+    """Calls a library function with device ``dev`` current; raises on an error code."""
+    global _get_device
     torch = _torch()
-    lib = _lib if _lib is not None else _load()
-    if torch.cuda.current_device() == dev:
-        rc = getattr(lib, name)(*args)
+    if _get_device is None:
+        # torch's raw getter, as for the stream
+        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    if _get_device() == dev:
+        rc = fn(*args)
     else:
         with torch.cuda.device(dev):
-            rc = getattr(lib, name)(*args)
+            rc = fn(*args)
     if rc:
         _check(name, rc)
+
+
+def _scratch(ws, nbytes, ref, dev):
+    # a tensor of its own for each call, so that calls on two streams, or captured in two graphs, never share one
+    torch = _torch()
+    if ws is None:
+        return ref.new_empty((max(nbytes, 16),), dtype=torch.uint8)
+    _require(ws, torch.uint8, "ws")
+    if ws.get_device() != dev:
+        raise ValueError("ws must be on the operands' device")
+    return ws
 
 
 def quantize_i8(src, out=None, scales=None):
     """bf16 or fp32 rows [R, K] -> (int8 codes [R, K], fp32 scales [R]): per-token codes of activations
     or per-channel codes of weights."""
     torch = _torch()
-    f32 = src.dtype is torch.float32
+    f32 = getattr(src, "dtype", None) is torch.float32
     r, k = _matrix(src, torch.float32 if f32 else torch.bfloat16, "src")
     dev = src.get_device()
     if out is None:
-        out = torch.empty((r, k), dtype=torch.int8, device=src.device)
+        out = torch.empty_like(src, dtype=torch.int8)
     if scales is None:
-        scales = torch.empty((r,), dtype=torch.float32, device=src.device)
-    _operands(dev, (out, torch.int8, (r, k), "out"), (scales, torch.float32, (r,), "scales"))
-    _call("stq1_quantize_i8", dev, src.data_ptr(), TYPE_F32 if f32 else TYPE_BF16, r, k, out.data_ptr(),
-          scales.data_ptr(), _stream(src))
+        scales = src.new_empty((r,), dtype=torch.float32)
+    lib = _lib if _lib is not None else _load()
+    _call("stq1_quantize_i8", dev, lib.stq1_quantize_i8, src.data_ptr(), TYPE_F32 if f32 else TYPE_BF16, r, k,
+          _operand(out, torch.int8, (r, k), dev, "out"), _operand(scales, torch.float32, (r,), dev, "scales"),
+          _stream(src))
     return out, scales
 
 
@@ -619,23 +635,13 @@ def i8_matmul(x_q, x_scales, w_q, w_scales, out=None, dtype=None):
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"i8_matmul gives torch.float32 or torch.bfloat16, not {dtype}")
     if out is None:
-        out = torch.empty((t, n), dtype=dtype, device=x_q.device)
-    _operands(dev, (x_scales, torch.float32, (t,), "x_scales"), (w_q, torch.int8, (n, k), "w_q"),
-              (w_scales, torch.float32, (n,), "w_scales"), (out, dtype, (t, n), "out"))
-    _call("stq1_i8_matmul", dev, x_q.data_ptr(), x_scales.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(),
-          out.data_ptr(), TYPE_F32 if dtype is torch.float32 else TYPE_BF16, t, n, k, _stream(x_q))
+        out = x_q.new_empty((t, n), dtype=dtype)
+    lib = _lib if _lib is not None else _load()
+    _call("stq1_i8_matmul", dev, lib.stq1_i8_matmul, x_q.data_ptr(),
+          _operand(x_scales, torch.float32, (t,), dev, "x_scales"), _operand(w_q, torch.int8, (n, k), dev, "w_q"),
+          _operand(w_scales, torch.float32, (n,), dev, "w_scales"), _operand(out, dtype, (t, n), dev, "out"),
+          TYPE_F32 if dtype is torch.float32 else TYPE_BF16, t, n, k, _stream(x_q))
     return out
-
-
-def _scratch(ws, nbytes, ref):
-    # a tensor of its own for each call, so that calls on two streams, or captured in two graphs, never share one
-    torch = _torch()
-    if ws is None:
-        return torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=ref.device)
-    _require(ws, torch.uint8, "ws")
-    if ws.get_device() != ref.get_device():
-        raise ValueError("ws must be on the operands' device")
-    return ws
 
 
 def i8_ffn(x, gateup_q, gateup_scales, down_q, down_scales, out=None, ws=None):
@@ -645,13 +651,15 @@ def i8_ffn(x, gateup_q, gateup_scales, down_q, down_scales, out=None, ws=None):
     n = _matrix(gateup_q, torch.int8, "gateup_q")[0]
     dev = x.get_device()
     if out is None:
-        out = torch.empty((t, h), dtype=torch.float32, device=x.device)
-    _operands(dev, (gateup_q, torch.int8, (n, h), "gateup_q"), (gateup_scales, torch.float32, (n,), "gateup_scales"),
-              (down_q, torch.int8, (h, n // 2), "down_q"), (down_scales, torch.float32, (h,), "down_scales"),
-              (out, torch.float32, (t, h), "out"))
-    ws = _scratch(ws, _load().stq1_i8_ffn_workspace(t, n, h), x)
-    _call("stq1_i8_ffn", dev, x.data_ptr(), gateup_q.data_ptr(), gateup_scales.data_ptr(), down_q.data_ptr(),
-          down_scales.data_ptr(), out.data_ptr(), t, n, h, ws.data_ptr(), ws.numel(), _stream(x))
+        out = torch.empty_like(x, dtype=torch.float32)
+    lib = _lib if _lib is not None else _load()
+    args = (x.data_ptr(), _operand(gateup_q, torch.int8, (n, h), dev, "gateup_q"),
+            _operand(gateup_scales, torch.float32, (n,), dev, "gateup_scales"),
+            _operand(down_q, torch.int8, (h, n // 2), dev, "down_q"),
+            _operand(down_scales, torch.float32, (h,), dev, "down_scales"),
+            _operand(out, torch.float32, (t, h), dev, "out"))
+    ws = _scratch(ws, lib.stq1_i8_ffn_workspace(t, n, h), x, dev)
+    _call("stq1_i8_ffn", dev, lib.stq1_i8_ffn, *args, t, n, h, ws.data_ptr(), ws.numel(), _stream(x))
     return out
 
 
@@ -664,13 +672,13 @@ def glu(x, w, save: bool = False, out=None, y=None):
     dev = x.get_device()
     save = save or y is not None
     if out is None:
-        out = torch.empty((t, n // 2), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((t, n // 2))
     if save and y is None:
-        y = torch.empty((t, n), dtype=torch.bfloat16, device=x.device)
-    _operands(dev, (w, torch.bfloat16, (n, k), "w"), (out, torch.bfloat16, (t, n // 2), "out"),
-              (y, torch.bfloat16, (t, n), "y"))
-    _call("stq1_glu", dev, x.data_ptr(), w.data_ptr(), out.data_ptr(), None if y is None else y.data_ptr(), t, n, k,
-          _stream(x))
+        y = x.new_empty((t, n))
+    lib = _lib if _lib is not None else _load()
+    _call("stq1_glu", dev, lib.stq1_glu, x.data_ptr(), _operand(w, torch.bfloat16, (n, k), dev, "w"),
+          _operand(out, torch.bfloat16, (t, n // 2), dev, "out"),
+          _operand(y, torch.bfloat16, (t, n), dev, "y") if save else None, t, n, k, _stream(x))
     return (out, y) if save else out
 
 
@@ -685,20 +693,20 @@ def glu_backward(dact, y, x, w, dx=None, dw=None, need_dx: bool = True, need_dw:
         raise ValueError("dx needs w, and dw needs x")
     k = _matrix(x, torch.bfloat16, "x")[1] if x is not None else _matrix(w, torch.bfloat16, "w")[1]
     dev = y.get_device()
-    if need_dx and dx is None:
-        dx = torch.empty((t, k), dtype=torch.bfloat16, device=y.device)
-    if need_dw and dw is None:
-        dw = torch.empty((n, k), dtype=torch.bfloat16, device=y.device)
-    if not need_dx:
-        dx = None
-    if not need_dw:
-        dw = None
-    _operands(dev, (dact, torch.bfloat16, (t, n // 2), "dact"), (x, torch.bfloat16, (t, k), "x"),
-              (w, torch.bfloat16, (n, k), "w"), (dx, torch.bfloat16, (t, k), "dx"), (dw, torch.bfloat16, (n, k), "dw"))
-    ws = _scratch(ws, _load().stq1_glu_backward_workspace(t, n, k), y)
-    ptr = lambda v: None if v is None else v.data_ptr()  # noqa: E731
-    _call("stq1_glu_backward", dev, dact.data_ptr(), y.data_ptr(), ptr(x), ptr(w), ptr(dx), ptr(dw), t, n, k,
-          ws.data_ptr(), ws.numel(), _stream(y))
+    # (empty_like is quicker than new_empty)
+    dx = None if not need_dx else dx if dx is not None else y.new_empty((t, k)) if x is None else torch.empty_like(x)
+    dw = None if not need_dw else dw if dw is not None else y.new_empty((n, k)) if w is None else torch.empty_like(w)
+    lib = _lib if _lib is not None else _load()
+    at = lambda v, shape, name: None if v is None else _operand(v, torch.bfloat16, shape, dev, name)  # noqa: E731
+    args = (_operand(dact, torch.bfloat16, (t, n // 2), dev, "dact"), y.data_ptr(), at(x, (t, k), "x"),
+            at(w, (n, k), "w"), at(dx, (t, k), "dx"), at(dw, (n, k), "dw"))
+    if ws is None:                                  # the workspace is dY: [T, N] bf16, as y
+        ws = torch.empty_like(y)
+        nbytes = t * n * 2
+    else:
+        ws = _scratch(ws, 0, y, dev)
+        nbytes = ws.numel()
+    _call("stq1_glu_backward", dev, lib.stq1_glu_backward, *args, t, n, k, ws.data_ptr(), nbytes, _stream(y))
     return dx, dw
 
 

@@ -2,7 +2,7 @@
 // Included by stq1_device.cu after its launch helpers.
 #pragma once
 
-#include "dense_gemv.cuh"
+#include "dense_few.cuh"
 #include "dense_tile.cuh"
 #include "glu_grad.cuh"
 #include "quant_i8.cuh"
@@ -11,7 +11,7 @@ namespace stq1 {
 namespace {
 
 constexpr long long kDenseMaxDim = 1LL << 30;
-constexpr int kFfnFusedTokens = 16;
+constexpr int kFfnFusedTokens = 4;
 constexpr long long kI8MaxK = 131056;    // 128 * 128 * K stays below 2^31
 
 bool dense_shape_ok(long long a, long long b, long long c) {
@@ -35,12 +35,28 @@ bool make_operand_map(CUtensorMap* map, const void* base, bool i8, long long row
 }
 
 std::atomic<bool> g_dense_configured[kMaxDevices];
+constexpr int kFewAllSmem = 232448;
+template <int EPI, bool QX, int MT, int NT>
+bool few_config_one() {
+  return cudaFuncSetAttribute(dense_few_kernel<EPI, QX, MT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kFewAllSmem) == cudaSuccess;
+}
+template <int EPI, bool QX>
+bool few_config() {
+  return few_config_one<EPI, QX, 2, 1>() && few_config_one<EPI, QX, 2, 2>() && few_config_one<EPI, QX, 4, 1>() &&
+         few_config_one<EPI, QX, 4, 2>();
+}
+template <int EPI, bool AMN, bool BMN, int S>
+bool split_config() {
+  return cudaFuncSetAttribute(dense_split_kernel<EPI, AMN, BMN, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kSplitSmemBytes) == cudaSuccess;
+}
 template <int EPI, bool AMN, bool BMN>
 bool dense_config() {
   return cudaFuncSetAttribute(dense_pair_kernel<EPI, AMN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kPairSmemBytes) == cudaSuccess &&
-         cudaFuncSetAttribute(dense_split_kernel<EPI, AMN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kSplitSmemBytes) == cudaSuccess;
+         split_config<EPI, AMN, BMN, 1>() && split_config<EPI, AMN, BMN, 2>() && split_config<EPI, AMN, BMN, 4>() &&
+         split_config<EPI, AMN, BMN, 8>();
 }
 int ensure_dense_configured() {
   const int dev = current_device();
@@ -50,6 +66,8 @@ int ensure_dense_configured() {
   if (g_dense_configured[dev].load(std::memory_order_relaxed)) return STQ1_OK;
   if (!(dense_config<kEpiI8F32, false, false>() && dense_config<kEpiI8Bf16, false, false>() &&
         dense_config<kEpiI8Glu, false, false>() && dense_config<kEpiGlu, false, false>() &&
+        few_config<kEpiI8F32, false>() && few_config<kEpiI8F32, true>() && few_config<kEpiI8Bf16, false>() &&
+        few_config<kEpiI8Glu, false>() && few_config<kEpiI8Glu, true>() && few_config<kEpiGlu, false>() &&
         dense_config<kEpiBf16, false, true>() && dense_config<kEpiBf16, true, true>())) {
     cudaGetLastError();
     return STQ1_ERR_CUDA;
@@ -88,7 +106,10 @@ int launch_tiles(const DenseProduct& d, cudaStream_t s) {
   const long long qm = (d.M + 127) / 128, qn = (rows_b + 127) / 128;
   const bool pair = qm * qn > sms;
   CUtensorMap ma, mb;
-  const int box_a = AMN ? 64 : 128, box_b = BMN || (GLU && !pair) ? 64 : 128;
+  // a lone row of tiles copies no more rows of A than there are (the sums of the others are never stored)
+  const int a_rows = !AMN && !pair && d.M < kDnRows ? static_cast<int>((d.M + 7) / 8 * 8) : kDnRows;
+  p.a_bytes = a_rows * kDnStepBytes;
+  const int box_a = AMN ? 64 : a_rows, box_b = BMN || (GLU && !pair) ? 64 : 128;
   if (!make_operand_map(&ma, d.a, I8, AMN ? d.K : d.M, AMN ? d.M : d.K, box_a) ||
       !make_operand_map(&mb, d.b, I8, BMN ? d.K : rows_b, BMN ? rows_b : d.K, box_b))
     return STQ1_ERR_CUDA;
@@ -103,36 +124,87 @@ int launch_tiles(const DenseProduct& d, cudaStream_t s) {
   p.tiles_n = static_cast<int>(qn);
   int S = 1;
   while (2 * S <= kSplitMax && 2 * S <= p.n_k && qm * qn * 2 * S <= sms) S *= 2;
-  return launch_pdl_cluster(dense_split_kernel<EPI, AMN, BMN>,
-                            dim3(static_cast<unsigned>(qm * qn), static_cast<unsigned>(S)), kSplitThreads,
-                            kSplitSmemBytes, s, static_cast<unsigned>(S), ma, mb, p);
+  auto launch = [&](auto kernel) {
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(qm * qn), static_cast<unsigned>(S)), kSplitThreads,
+                              kSplitSmemBytes, s, static_cast<unsigned>(S), ma, mb, p);
+  };
+  switch (S) {
+    case 1: return launch(dense_split_kernel<EPI, AMN, BMN, 1>);
+    case 2: return launch(dense_split_kernel<EPI, AMN, BMN, 2>);
+    case 4: return launch(dense_split_kernel<EPI, AMN, BMN, 4>);
+    default: return launch(dense_split_kernel<EPI, AMN, BMN, 8>);
+  }
 }
+
+// How a product with few tokens is laid out: outputs per CTA so that every SM
+// has one CTA's share, and as many steps in flight per warp as fit.
+struct FewPlan {
+  int rows, pad, n_k, n_slots;
+  size_t smem;
+};
+bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu) {
+  if (T > kFewMaxTokens) return false;
+  const int sms = sm_count(), unit = glu ? 8 : 16;         // the gate rows end on a whole swizzle atom
+  f->rows = static_cast<int>(std::min<long long>(glu ? 32 : 64, (N + sms - 1) / sms));
+  f->pad = (f->rows + unit - 1) / unit * unit * (glu ? 2 : 1);
+  f->n_k = static_cast<int>((kbytes + kDnStepBytes - 1) / kDnStepBytes);
+  const long long x = few_pitch(f->n_k) * T;
+  const long long per_warp = (f->n_k + kFewWarps - 1) / kFewWarps;
+  const long long round = static_cast<long long>(f->pad) * kDnStepBytes * kFewWarps;     // one slot per warp
+  const long long slots = std::min<long long>(std::min<long long>((kFewAllSmem - 1024 - kFewHead - x) / round, per_warp),
+                                              kFewMaxSlots);
+  if (slots < 1 || (slots < 2 && per_warp > 1)) return false;
+  f->n_slots = static_cast<int>(slots);
+  const int mt = f->pad > 32 ? 4 : 2, nt = T > 8 ? 2 : 1;
+  const long long sums = 512LL * kFewWarps * mt * nt;      // the warps' sums take the place of slots and tokens
+  f->smem = static_cast<size_t>(1024 + kFewHead + std::max(slots * round + x, sums));
+  return true;
+}
+
+// What ran or runs around a streaming product: `early`, the kernel before does
+// not write its weights; `next`, the weights that the kernel after reads.
+struct FewChain {
+  bool early;
+  const void* next;
+  long long next_bytes;
+};
 
 template <int EPI, bool QX>
-int launch_gemv(const GemvArgs& p, cudaStream_t s) {
-  const long long per = epi_glu(EPI) ? 8 : 16;
-  const unsigned grid = static_cast<unsigned>((p.N + per - 1) / per);
-  if (p.T <= 8) return launch_pdl(dense_gemv_kernel<EPI, QX, 1, 4>, grid, kGvThreads, 0, s, p);
-  if (p.T <= 16) return launch_pdl(dense_gemv_kernel<EPI, QX, 2, 4>, grid, kGvThreads, 0, s, p);
-  return launch_pdl(dense_gemv_kernel<EPI, QX, 4, 2>, grid, kGvThreads, 0, s, p);
+int launch_few(const FewPlan& f, const DenseProduct& d, const FewChain& c, cudaStream_t s) {
+  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
+  int rc = ensure_dense_configured();
+  if (rc != STQ1_OK) return rc;
+  FewArgs p{};
+  p.x = d.a;
+  p.sx = d.sx;
+  p.sw = d.sw;
+  p.out = d.out;
+  p.y = d.y;
+  p.N = d.N;
+  p.K = d.K;
+  p.T = static_cast<int>(d.M);
+  p.rows = f.rows;
+  p.pad = f.pad;
+  p.n_k = f.n_k;
+  p.n_slots = f.n_slots;
+  p.early = c.early;
+  p.next = static_cast<const char*>(c.next);
+  p.next_bytes = c.next_bytes;
+  CUtensorMap mw;
+  if (!make_operand_map(&mw, d.b, I8, GLU ? 2 * d.N : d.N, d.K, f.rows)) return STQ1_ERR_CUDA;
+  const unsigned grid = static_cast<unsigned>((d.N + f.rows - 1) / f.rows);
+  auto launch = [&](auto kernel) { return launch_pdl(kernel, grid, kFewThreads, f.smem, s, mw, p); };
+  if (f.pad > 32)
+    return d.M > 8 ? launch(dense_few_kernel<EPI, QX, 4, 2>) : launch(dense_few_kernel<EPI, QX, 4, 1>);
+  return d.M > 8 ? launch(dense_few_kernel<EPI, QX, 2, 2>) : launch(dense_few_kernel<EPI, QX, 2, 1>);
 }
 
-// A product of K-major operands: few tokens take the gemv kernel.
+// A product of K-major operands: few tokens take the streaming kernel.
 template <int EPI>
 int launch_product(const DenseProduct& d, cudaStream_t s) {
-  if (d.M <= kGvMaxTokens) {
-    GemvArgs g{};
-    g.w = d.b;
-    g.x = d.a;
-    g.sx = d.sx;
-    g.sw = d.sw;
-    g.out = d.out;
-    g.y = d.y;
-    g.N = d.N;
-    g.K = d.K;
-    g.T = static_cast<int>(d.M);
-    return launch_gemv<EPI, false>(g, s);
-  }
+  FewPlan f;
+  if (plan_few(&f, d.M, d.N, d.K * (epi_i8(EPI) ? 1 : 2), epi_glu(EPI)))
+    return launch_few<EPI, false>(f, d, FewChain{}, s);
   return launch_tiles<EPI, false, false>(d, s);
 }
 
@@ -256,31 +328,31 @@ extern "C" int stq1_i8_ffn(const uint16_t* x, const int8_t* gateup_q, const floa
   uint16_t* act = reinterpret_cast<uint16_t*>(wsb + f.act_off);
   int8_t* aq = reinterpret_cast<int8_t*>(wsb + f.aq_off);
   float* sa = reinterpret_cast<float*>(wsb + f.sa_off);
-  if (T <= kFfnFusedTokens) {
-    // codes made inside the products: two launches
-    GemvArgs g{};
-    g.w = gateup_q;
-    g.x = x;
-    g.sw = gateup_scales;
-    g.out = act;
-    g.N = N / 2;
-    g.K = H;
-    g.T = static_cast<int>(T);
-    int rc = launch_gemv<kEpiI8Glu, true>(g, s);
-    if (rc != STQ1_OK) return rc;
-    g.w = down_q;
-    g.x = act;
-    g.sw = down_scales;
-    g.out = out;
-    g.N = H;
-    g.K = N / 2;
-    return launch_gemv<kEpiI8F32, true>(g, s);
+  const DenseProduct up = i8_product(xq, sx, gateup_q, gateup_scales, act, T, N / 2, H);
+  const DenseProduct down = i8_product(aq, sa, down_q, down_scales, out, T, H, N / 2);
+  FewPlan fg, fd;
+  if (plan_few(&fg, T, N / 2, H, true) && plan_few(&fd, T, H, N / 2, false)) {
+    // few tokens: each kernel streams its weights while the one before it
+    // still runs, and the first brings the second's into L2
+    const FewChain c1{false, down_q, static_cast<long long>(H) * (N / 2)}, c2{true, nullptr, 0};
+    int rc;
+    if (T <= kFfnFusedTokens) {           // codes made inside the products: two launches
+      DenseProduct u = up, dn = down;
+      u.a = x;
+      dn.a = act;
+      rc = launch_few<kEpiI8Glu, true>(fg, u, c1, s);
+      return rc != STQ1_OK ? rc : launch_few<kEpiI8F32, true>(fd, dn, c2, s);
+    }
+    rc = launch_quant_i8(x, STQ1_TYPE_BF16, T, H, xq, sx, s);
+    if (rc == STQ1_OK) rc = launch_few<kEpiI8Glu, false>(fg, up, FewChain{true, c1.next, c1.next_bytes}, s);
+    if (rc == STQ1_OK) rc = launch_quant_i8(act, STQ1_TYPE_BF16, T, N / 2, aq, sa, s);
+    return rc != STQ1_OK ? rc : launch_few<kEpiI8F32, false>(fd, down, c2, s);
   }
   int rc = launch_quant_i8(x, STQ1_TYPE_BF16, T, H, xq, sx, s);
   if (rc != STQ1_OK) return rc;
-  rc = launch_product<kEpiI8Glu>(i8_product(xq, sx, gateup_q, gateup_scales, act, T, N / 2, H), s);
+  rc = launch_product<kEpiI8Glu>(up, s);
   if (rc != STQ1_OK) return rc;
   rc = launch_quant_i8(act, STQ1_TYPE_BF16, T, N / 2, aq, sa, s);
   if (rc != STQ1_OK) return rc;
-  return launch_product<kEpiI8F32>(i8_product(aq, sa, down_q, down_scales, out, T, H, N / 2), s);
+  return launch_product<kEpiI8F32>(down, s);
 }

@@ -1,0 +1,294 @@
+// Products of the 8-bit integer and bf16 gated layers with up to 16 tokens:
+// the weights are streamed once from HBM, everything else is kept small.
+//
+// A CTA owns a few weight rows (about N / SMs of them, so that every SM pulls
+// its share) over the whole of K: no exchange between CTAs.  Its eight warps
+// share out the 128-byte steps of K; each brings its own steps by tensor
+// copies into slots of its own and contracts them with mma.sync.  (tcgen05
+// is no help here: an MMA reads 64 or 128 rows of A whatever the tokens, and
+// with 32 weight rows a step's four MMAs take longer than its bytes from HBM:
+// 13 us against 7 on [4096, 7168].)
+//
+// A contraction may take its k in any order as long as both operands agree on
+// it.  So a lane's share of an A fragment need not be the 4-byte pieces that
+// mma.sync's layout spreads over a row: lane (g, t) takes the 16-byte pieces
+// 2t and 2t + 1 of a step's rows g and g + 8 (words 0, 1 and 2, 3 of a piece
+// feed one MMA each), and the same pieces of token g make the B fragments.
+// In the copies' 128-byte swizzle the reads of a quarter warp (two rows, every
+// second piece) fall on different banks.  8-bit and bf16 operands have the
+// same word layout.
+//
+// For the gated forms a fragment's rows 0-7 are gate rows and its rows 8-15
+// the up rows of the same outputs: a lane then holds g and u of one output.
+#pragma once
+
+#include "dense_math.cuh"
+#include "dense_tile.cuh"
+#include "quant_i8.cuh"
+
+namespace stq1 {
+
+constexpr int kFewMaxTokens = 16;
+constexpr int kFewWarps = 8;
+constexpr int kFewThreads = 32 * kFewWarps;
+constexpr int kFewMaxSlots = 8;              // steps in flight per warp
+constexpr int kFewHead = 1024;               // barriers and small arrays
+
+struct FewArgs {
+  const void* x;               // [T, K] codes or bf16
+  const float *sx, *sw;
+  void* out;
+  uint16_t* y;
+  long long N, K;              // outputs (for the gated forms half of the weight rows); values per row
+  int T;
+  int rows;                    // outputs per CTA
+  int pad;                     // weight rows of one step in shared memory (a multiple of 16)
+  int n_k;                     // 128-byte steps of K
+  int n_slots;
+  int early;                   // the weights are not written by the kernel before: load them at once
+  const char* next;            // weights of the kernel after, brought into L2 at the end, or NULL
+  long long next_bytes;
+};
+
+// Bytes between tokens in shared memory: whole steps and 16 more, so that two
+// tokens' pieces (every second one of a step) fall on different banks.
+__host__ __device__ constexpr long long few_pitch(int n_k) { return n_k * 128LL + 16; }
+
+__device__ __forceinline__ void few_mma(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void few_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// QX: x is bf16 and its codes are made here: each CTA finds the tokens' scales
+// itself, T * K values from L2, while its first weights are on their way.
+// MT: fragments of 16 weight rows (at most); NT: groups of 8 tokens.
+template <int EPI, bool QX, int MT, int NT>
+__global__ void __launch_bounds__(kFewThreads, 2)
+dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
+  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
+  static_assert(I8 || !QX, "codes are made for 8-bit weights");
+  using Acc = std::conditional_t<I8, int, float>;
+  constexpr int ES = I8 ? 1 : 2;
+  constexpr int kStep = kDnStepBytes / ES;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const uint32_t sraw = smem_u32(smem_raw);
+  const uint32_t sbase = (sraw + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t s_max = sbase + 8 * kFewMaxSlots * kFewWarps, s_scale = s_max + 32, bar_x = s_scale + 64;
+  const uint32_t slot_bytes = p.pad * kDnStepBytes;
+  const uint32_t s_w = sbase + kFewHead;                               // the warps' slots
+  const uint32_t s_x = s_w + kFewWarps * p.n_slots * slot_bytes;       // the tokens
+  const uint32_t pitch = static_cast<uint32_t>(few_pitch(p.n_k));
+  const uint32_t my_bar = sbase + 8 * kFewMaxSlots * warp;
+  const uint32_t my_slots = s_w + warp * p.n_slots * slot_bytes;
+  const long long n0 = static_cast<long long>(blockIdx.x) * p.rows;
+
+  // ---- this warp's first steps ----
+  const int y0 = static_cast<int>(n0), y1 = static_cast<int>(p.N + n0);
+  const uint32_t step_bytes = (GLU ? 2 : 1) * p.rows * kDnStepBytes;
+  auto fetch = [&](int step, int slot) {                               // lane 0 only
+    const uint32_t bar = my_bar + 8 * slot, dst = my_slots + slot * slot_bytes;
+    mbar_arrive_expect_tx(bar, step_bytes);
+    dn_load<1>(dst, &map_w, step * kStep, y0, bar);
+    if constexpr (GLU) dn_load<1>(dst + slot_bytes / 2, &map_w, step * kStep, y1, bar);
+  };
+  if (lane == 0) {
+    for (int i = 0; i < p.n_slots; ++i) mbar_init(my_bar + 8 * i, 1);
+    if (warp == 0) mbar_init(bar_x, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  // With `early` the weights are fetched while the kernel before still runs:
+  // what ran before that one is complete (its CTAs passed their own wait
+  // before they let this kernel start), and the weights are not its output.
+  if (!p.early) griddep_wait();
+  if (lane == 0)
+    for (int i = 0; i < p.n_slots && warp + kFewWarps * i < p.n_k; ++i) fetch(warp + kFewWarps * i, i);
+  if (p.early) griddep_wait();
+  griddep_launch_dependents();
+  // Once a warp has asked for its last step, it asks for its share of the next
+  // kernel's weights in L2, so that HBM does not rest between the two.
+  auto prefetch_next = [&]() {                                         // lane 0 only
+    const long long share = (p.next_bytes / (static_cast<long long>(gridDim.x) * kFewWarps) + 16) & ~15LL;
+    long long at = share * (blockIdx.x * static_cast<long long>(kFewWarps) + warp);
+    const long long end = min(at + share, p.next_bytes);
+    for (; at < end; at += 4096)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.next + at),
+                   "r"(static_cast<uint32_t>(min(4096LL, end - at)))
+                   : "memory");
+  };
+  if (lane == 0 && p.next && warp + kFewWarps * p.n_slots >= p.n_k) prefetch_next();
+
+  // ---- the tokens into shared memory ----
+  const long long kbytes = p.K * ES;
+  if constexpr (QX) {
+    // 8 / n warps per token, n = T rounded up to a power of two (two rounds for more than 8 tokens)
+    const int n = p.T <= 1 ? 1 : (p.T <= 2 ? 2 : (p.T <= 4 ? 4 : 8));
+    const int per = kFewWarps / n, first = (warp % per) * 32 + lane;
+    const int nv = static_cast<int>(p.K / 16);
+    for (int tok0 = 0; tok0 < p.T; tok0 += 8) {
+      const int tok = tok0 + warp / per;
+      const char* xr = static_cast<const char*>(p.x) + tok * p.K * 2;
+      uint32_t m = 0u;
+      if (tok < p.T) {
+#pragma unroll 4
+        for (int i = first; i < nv; i += 32 * per) {
+          Row8<false> a, b;
+          a.load(xr, 2 * i);
+          b.load(xr, 2 * i + 1);
+          m = max(m, max(a.amax_bits(), b.amax_bits()));
+        }
+      }
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (per > 1) {
+        if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(s_max + 4 * warp), "r"(m) : "memory");
+        __syncthreads();
+        for (int i = 0; i < per; ++i) {
+          uint32_t o;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(o) : "r"(s_max + 4 * (warp / per * per + i)));
+          m = max(m, o);
+        }
+      }
+      const I8Scale sc = i8_scale(m);
+      if (tok < p.T) {
+        if (first == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_scale + 4 * tok), "f"(sc.scale) : "memory");
+#pragma unroll 4
+        for (int i = first; i < nv; i += 32 * per) {
+          Row8<false> a, b;
+          a.load(xr, 2 * i);
+          b.load(xr, 2 * i + 1);
+          const uint2 lo = a.codes(sc.inv), hi = b.codes(sc.inv);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(s_x + tok * pitch + 16 * i), "r"(lo.x), "r"(lo.y),
+                       "r"(hi.x), "r"(hi.y)
+                       : "memory");
+        }
+      }
+    }
+  } else {
+    // one bulk copy per token (K * ES and the pitch are multiples of 16 bytes)
+    if (threadIdx.x == 0) {
+      mbar_arrive_expect_tx(bar_x, static_cast<uint32_t>(p.T * kbytes));
+      for (int tok = 0; tok < p.T; ++tok)
+        bulk_g2s(s_x + tok * pitch, static_cast<const char*>(p.x) + tok * kbytes, static_cast<uint32_t>(kbytes), bar_x);
+    }
+  }
+  {
+    // K past its end within the last step: the weights read as zero there, and so must the tokens (0 * NaN)
+    const int end = static_cast<int>(kbytes / 16), tail = p.n_k * 8 - end;
+    for (int i = threadIdx.x; i < tail * p.T; i += kFewThreads)
+      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(s_x + (i / tail) * pitch + 16 * (end + i % tail)), "r"(0u)
+                   : "memory");
+  }
+  __syncthreads();
+  bool ok = QX || mbar_wait_bounded(bar_x, 0);
+
+  // ---- this warp's steps ----
+  const int mt = p.pad >> 4;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  Acc acc[MT][NT][4] = {};
+  // rows of a fragment in a slot, and this lane's pieces of them
+  const uint32_t up = GLU ? slot_bytes / 2 : 8 * kDnStepBytes;         // from row g to the row of fragment row g + 8
+  const uint32_t frag = (GLU ? 8 : 16) * kDnStepBytes;
+  const uint32_t off0 = g * kDnStepBytes + (((2 * t) ^ g) << 4), off1 = g * kDnStepBytes + (((2 * t + 1) ^ g) << 4);
+  int slot = 0;
+  uint32_t ph = 0;
+  for (int step = warp; ok && step < p.n_k; step += kFewWarps) {
+    if (!mbar_wait_bounded(my_bar + 8 * slot, ph)) {
+      ok = false;
+      break;                                         // (its own copies have had that wait to land)
+    }
+    uint4 x0[NT], x1[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const bool token = 8 * n + g < p.T;
+      const uint32_t at = s_x + (8 * n + g) * pitch + step * kDnStepBytes + 32 * t;
+      x0[n] = token ? lds_v4(at) : zero;
+      x1[n] = token ? lds_v4(at + 16) : zero;
+    }
+    const uint32_t base = my_slots + slot * slot_bytes;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      if (i < mt) {
+        const uint32_t b = base + i * frag;
+        const uint4 a0 = lds_v4(b + off0), a1 = lds_v4(b + up + off0);
+        const uint4 c0 = lds_v4(b + off1), c1 = lds_v4(b + up + off1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          few_mma(acc[i][n], a0.x, a1.x, a0.y, a1.y, x0[n].x, x0[n].y);
+          few_mma(acc[i][n], a0.z, a1.z, a0.w, a1.w, x0[n].z, x0[n].w);
+          few_mma(acc[i][n], c0.x, c1.x, c0.y, c1.y, x1[n].x, x1[n].y);
+          few_mma(acc[i][n], c0.z, c1.z, c0.w, c1.w, x1[n].z, x1[n].w);
+        }
+      }
+    }
+    __syncwarp();                                    // every lane has read the slot
+    const int next = step + kFewWarps * p.n_slots;
+    if (lane == 0 && next < p.n_k) {
+      fetch(next, slot);
+      if (p.next && next + kFewWarps >= p.n_k) prefetch_next();
+    }
+    if (++slot == p.n_slots) slot = 0, ph ^= 1;
+  }
+  __syncthreads();                                   // the slots are free: the warps' sums take their place
+  const uint32_t red = s_w + (warp * MT * NT * 32 + lane) * 16;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(red + (i * NT + n) * 512),
+                   "r"(*reinterpret_cast<const uint32_t*>(&acc[i][n][0])), "r"(*reinterpret_cast<const uint32_t*>(&acc[i][n][1])),
+                   "r"(*reinterpret_cast<const uint32_t*>(&acc[i][n][2])), "r"(*reinterpret_cast<const uint32_t*>(&acc[i][n][3]))
+                   : "memory");
+  if (__syncthreads_or(!ok)) return;                 // a wait ran out (flagged): nothing is stored
+
+  // sums over the warps, in their order; consecutive threads take consecutive outputs of one token
+  const int count = static_cast<int>(min(static_cast<long long>(p.rows), p.N - n0));
+  for (int e = threadIdx.x; e < count * p.T; e += kFewThreads) {
+    const int tok = e / count, r = e - tok * count;
+    const int i = GLU ? r >> 3 : r >> 4;
+    const uint32_t at = s_w + ((i * NT + (tok >> 3)) * 32 + (r & 7) * 4 + ((tok & 7) >> 1)) * 16 + 4 * (tok & 1);
+    auto total = [&](int reg) {
+      Acc v;
+#pragma unroll
+      for (int q = 0; q < kFewWarps; ++q) {
+        uint32_t w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at + 4 * reg + q * MT * NT * 512));
+        const Acc a = *reinterpret_cast<const Acc*>(&w);
+        if (q == 0) v = a;
+        else v += a;
+      }
+      return v;
+    };
+    const long long n = n0 + r;
+    float sx = 0.f;
+    if constexpr (QX) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sx) : "r"(s_scale + 4 * tok));
+    else if constexpr (I8) sx = p.sx[tok];
+    auto value = [&](Acc v, long long row) -> float {
+      if constexpr (I8) return i8_value(v, sx, p.sw[row]);
+      else return v;
+    };
+    if constexpr (GLU) {
+      const float gv = value(total(0), n), uv = value(total(2), p.N + n);
+      static_cast<uint16_t*>(p.out)[tok * p.N + n] = static_cast<uint16_t>(swiglu_bf16(gv, uv));
+      if constexpr (EPI == kEpiGlu)
+        if (p.y) {
+          p.y[tok * 2 * p.N + n] = static_cast<uint16_t>(bf16_bits_rn(gv));
+          p.y[tok * 2 * p.N + p.N + n] = static_cast<uint16_t>(bf16_bits_rn(uv));
+        }
+    } else {
+      const float v = value(total((r & 8) ? 2 : 0), n);
+      if constexpr (EPI == kEpiI8F32) static_cast<float*>(p.out)[tok * p.N + n] = v;
+      else static_cast<uint16_t*>(p.out)[tok * p.N + n] = static_cast<uint16_t>(bf16_bits_rn(v));
+    }
+  }
+}
+
+}  // namespace stq1

@@ -58,26 +58,78 @@ __device__ __forceinline__ float i8_value(int acc, float sx, float sw) {
 }
 
 // ---- the gated activation ----
-__device__ __noinline__ uint32_t swiglu_bf16_slow(float g, float u) {
+// bf16 bits of SiLU(g) * u, rounded once: the bits that swiglu_kernel's fp64
+// evaluation gives, in three steps.
+//
+// 1. fp32: expf (1 unit in the last place), the sum (1/2), the division (2)
+//    and the product (1/2) are together off by at most 4 halves of a binade's
+//    unit, so by less than 9 units of the result.  It decides the rounding
+//    unless its lower half lies within 9 units of the midpoint: one value in
+//    about 3400.
+// 2. Those, in fp64 by a short evaluation good to 2^-44: e^-g as 2^k times the
+//    Taylor polynomial on |r| <= ln(2) / 2 (r^12 / 12! < 2^-47), the
+//    reciprocal by one Newton step from fp32's.  Short, because a warp comes
+//    here about once per tile: with exp, a division and a general rounding the
+//    instruction fetches alone took the 4096-token int8 layer from 163 to 196 us.
+// 3. Values near the ends of fp32's range and NaN as swiglu_kernel does.
+__device__ __noinline__ uint32_t swiglu_bf16_ends(float g, float u) {
   const double gd = g;
   return bf16_bits_from_f64(gd / (1.0 + exp(-gd)) * static_cast<double>(u));
 }
-
-// bf16 bits of SiLU(g) * u, rounded once: the bits that swiglu_kernel's fp64
-// evaluation gives.  In fp32, expf, the sum, the division and the product are
-// together off by less than 8 units in the last place (1.01 + 0.5 + 2 + 0.5 of
-// them, the division's approximation being good to 2), so the fp32 result decides the bf16 rounding unless its lower half lies
-// within 16 units of the midpoint.  Those values (one in about 2000), the ones
-// near the ends of fp32's range and NaN are evaluated in fp64.
-__device__ __forceinline__ uint32_t swiglu_bf16(float g, float u) {
+__device__ __noinline__ uint32_t swiglu_bf16_border(float g, float u) {
+  const double x = -static_cast<double>(g);
+  const int k = __float2int_rn(g * -1.44269504f);
+  const double r = fma(static_cast<double>(k), -0.693147180559945309, x);
+  double e = 1.0 / 39916800.0;                       // 1 / 11!
+#pragma unroll
+  for (int n = 11; n >= 1; --n) {
+    constexpr double kInvFact[11] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040,
+                                     1.0 / 40320, 1.0 / 362880, 1.0 / 3628800};
+    e = fma(e, r, kInvFact[n - 1]);
+  }
+  e = __hiloint2double(__double2hiint(e) + (k << 20), __double2loint(e));
+  const double d = 1.0 + e;
+  double rc = static_cast<double>(__frcp_rn(static_cast<float>(d)));
+  rc = fma(rc, fma(-d, rc, 1.0), rc);
+  const double v = static_cast<double>(g) * static_cast<double>(u) * rc;
+  // 19 bits: sign, 11 of exponent, 7 of mantissa, rounded to nearest, ties to even
+  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v));
+  const uint32_t q = static_cast<uint32_t>((b + ((1ull << 44) - 1) + ((b >> 45) & 1)) >> 45);
+  return ((q & 0x3FFFFu) - (896u << 7)) | ((q >> 18) << 15);
+}
+// The fp32 step: bits rounded from v; false where another step must decide.
+__device__ __forceinline__ bool swiglu_bf16_fast(float g, float u, uint32_t& bits) {
   const float s = __fdividef(g, 1.f + expf(-g));
   const float v = s * u;
   const uint32_t b = __float_as_uint(v);
-  const uint32_t low = b & 0xFFFFu;
-  const bool clear = low - 0x7FF0u > 0x20u;
-  if (clear && fabsf(s) > 1e-30f && fabsf(v) > 1e-30f && fabsf(v) < 1e38f)
-    return (b + 0x7FFFu + ((b >> 16) & 1u)) >> 16;
-  return swiglu_bf16_slow(g, u);
+  bits = (b + 0x7FFFu + ((b >> 16) & 1u)) >> 16;
+  return fabsf(s) > 1e-30f && fabsf(v) > 1e-30f && fabsf(v) < 1e38f && (b & 0xFFFFu) - 0x7FF7u > 18u;
+}
+__device__ __noinline__ uint32_t swiglu_bf16_slow(float g, float u) {
+  const float s = __fdividef(g, 1.f + expf(-g)), v = s * u;
+  if (fabsf(s) > 1e-30f && fabsf(v) > 1e-30f && fabsf(v) < 1e38f) return swiglu_bf16_border(g, u);
+  return swiglu_bf16_ends(g, u);
+}
+__device__ __forceinline__ uint32_t swiglu_bf16(float g, float u) {
+  uint32_t bits;
+  return swiglu_bf16_fast(g, u, bits) ? bits : swiglu_bf16_slow(g, u);
+}
+// N values, two to a word: the fp32 steps without a branch between them, so
+// that their latencies overlap, then the few that need more.  (A branch per
+// value left the 4096-token int8 layer's epilogue longer than its MMAs.)
+template <int N>
+__device__ __forceinline__ void swiglu_bf16_pack(const float (&g)[N], const float (&u)[N], uint32_t* words) {
+  uint32_t slow = 0;
+  uint32_t bits[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) slow |= swiglu_bf16_fast(g[i], u[i], bits[i]) ? 0u : 1u << i;
+  if (__any_sync(0xffffffffu, slow != 0)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((slow >> i) & 1u) bits[i] = swiglu_bf16_slow(g[i], u[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; i += 2) words[i / 2] = bits[i] | (bits[i + 1] << 16);
 }
 
 __device__ __forceinline__ uint32_t bf16_bits_rn(float v) {

@@ -29,6 +29,7 @@ __host__ __device__ constexpr bool epi_glu(int e) { return e == kEpiI8Glu || e =
 struct DenseArgs {
   long long M, N;                    // outputs; for the gated forms N is half of B's rows
   int n_k;                           // 128-byte steps of K
+  int a_bytes;                       // bytes of A per step (split kernel)
   int tiles_m, tiles_n;
   const float *sx, *sw;              // int8: scales of A's rows and of B's rows
   void* out;                         // [M, N]
@@ -353,18 +354,18 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             swu = col_scale(p.N, col0 + 16 * c);
           }
           tmem_wait_ld();
+          float gv[16], uv[16];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float gv[2], uv[2];
+          for (int i = 0; i < 16; ++i) {
+            gv[i] = dn_sum<I8>(g[i], sx, I8 ? __shfl_sync(0xffffffffu, swg, i) : 0.f);
+            uv[i] = dn_sum<I8>(u[i], sx, I8 ? __shfl_sync(0xffffffffu, swu, i) : 0.f);
+          }
+          swiglu_bf16_pack<16>(gv, uv, act + 8 * c);
+          if constexpr (EPI == kEpiGlu) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              gv[h] = dn_sum<I8>(g[i + h], sx, I8 ? __shfl_sync(0xffffffffu, swg, i + h) : 0.f);
-              uv[h] = dn_sum<I8>(u[i + h], sx, I8 ? __shfl_sync(0xffffffffu, swu, i + h) : 0.f);
-            }
-            act[8 * c + i / 2] = swiglu_bf16(gv[0], uv[0]) | (swiglu_bf16(gv[1], uv[1]) << 16);
-            if constexpr (EPI == kEpiGlu) {
-              kg[8 * c + i / 2] = bf16_bits_rn(gv[0]) | (bf16_bits_rn(gv[1]) << 16);
-              ku[8 * c + i / 2] = bf16_bits_rn(uv[0]) | (bf16_bits_rn(uv[1]) << 16);
+            for (int i = 0; i < 16; i += 2) {
+              kg[8 * c + i / 2] = bf16_bits_rn(gv[i]) | (bf16_bits_rn(gv[i + 1]) << 16);
+              ku[8 * c + i / 2] = bf16_bits_rn(uv[i]) | (bf16_bits_rn(uv[i + 1]) << 16);
             }
           }
         }
@@ -441,7 +442,7 @@ static_assert(kDnRows * kSplitPitch * 4 <= kSplitOffBar, "a finished piece takes
 // the 128 x 128 sums into its shared memory; each then adds up its share of
 // the rows over all pieces, in the order of the pieces, and stores them: the
 // result does not depend on which CTA comes first.
-template <int EPI, bool AMN, bool BMN>
+template <int EPI, bool AMN, bool BMN, int S>
 __global__ void __launch_bounds__(kSplitThreads, 1)
 dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const DenseArgs p) {
@@ -452,7 +453,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   const uint32_t bar = sbase + kSplitOffBar;
   const uint32_t bar_full = bar, bar_empty = bar + 64, bar_acc = bar + 128, s_tmem = bar + 144;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = gridDim.y, piece = blockIdx.y;       // the cluster runs along y
+  const int piece = blockIdx.y;                      // the cluster of S runs along y
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSplitStages; ++i) {
       mbar_init(bar_full + 8 * i, 1);
@@ -481,7 +482,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       for (int k = k0; k < k1; ++k) {
         const uint32_t it = k - k0, s = it % kSplitStages, use = it / kSplitStages;
         if (!mbar_wait_bounded(bar_empty + 8 * s, (use & 1) ^ 1)) break;
-        mbar_arrive_expect_tx(bar_full + 8 * s, kDnStageBytes);
+        mbar_arrive_expect_tx(bar_full + 8 * s, p.a_bytes + kDnOperandBytes);
         const uint32_t dst = sbase + s * kDnStageBytes, b = bar_full + 8 * s;
         dn_load_operand<I8, AMN, 1>(dst, &map_a, k, tm * kDnRows, b);
         if constexpr (GLU) {
@@ -551,23 +552,30 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   }
   for (int r = piece + S * warp; r < rows; r += S * (kSplitThreads / 32)) {
     const uint32_t at = sbase + r * (kSplitPitch * 4);
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    uint32_t w[S][4], v[4];
+#pragma unroll
     for (int q = 0; q < S; ++q) {
       const uint32_t src = dn_mapa(at, q);
-      uint32_t w[4];
       if constexpr (GLU) {
-        asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src + 8 * lane) : "memory");
-        asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "r"(src + 256 + 8 * lane) : "memory");
+        asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(w[q][0]), "=r"(w[q][1]) : "r"(src + 8 * lane) : "memory");
+        asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];"
+                     : "=r"(w[q][2]), "=r"(w[q][3])
+                     : "r"(src + 256 + 8 * lane)
+                     : "memory");
       } else {
         asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3])
                      : "r"(src + 16 * lane)
                      : "memory");
       }
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (I8) v[i] += w[i];
-        else v[i] = q == 0 ? w[i] : __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+    for (int i = 0; i < 4; ++i) {
+      v[i] = w[0][i];
+#pragma unroll
+      for (int q = 1; q < S; ++q) {
+        if constexpr (I8) v[i] += w[q][i];
+        else v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[q][i]));
       }
     }
     const long long m = m0 + r;
