@@ -577,17 +577,22 @@ def _operand(t, dtype, shape, dev, name):
 _get_device = None
 
 
-def _call(name: str, dev: int, fn, *args):
-    """Calls a library function with device ``dev`` current; raises on an error code."""
+def _current_device() -> int:
     global _get_device
-    torch = _torch()
     if _get_device is None:
         # torch's raw getter, as for the stream
+        torch = _torch()
         _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-    if _get_device() == dev:
+    return _get_device()
+
+
+def _call(name: str, dev: int, *args):
+    """Calls a library function with device ``dev`` current; raises on an error code."""
+    fn = getattr(_lib if _lib is not None else _load(), name)
+    if _current_device() == dev:
         rc = fn(*args)
     else:
-        with torch.cuda.device(dev):
+        with _torch().cuda.device(dev):
             rc = fn(*args)
     if rc:
         _check(name, rc)
@@ -615,8 +620,7 @@ def quantize_i8(src, out=None, scales=None):
         out = torch.empty_like(src, dtype=torch.int8)
     if scales is None:
         scales = src.new_empty((r,), dtype=torch.float32)
-    lib = _lib if _lib is not None else _load()
-    _call("stq1_quantize_i8", dev, lib.stq1_quantize_i8, src.data_ptr(), TYPE_F32 if f32 else TYPE_BF16, r, k,
+    _call("stq1_quantize_i8", dev, src.data_ptr(), TYPE_F32 if f32 else TYPE_BF16, r, k,
           _operand(out, torch.int8, (r, k), dev, "out"), _operand(scales, torch.float32, (r,), dev, "scales"),
           _stream(src))
     return out, scales
@@ -628,7 +632,7 @@ def i8_matmul(x_q, x_scales, w_q, w_scales, out=None, dtype=None):
     dtype: torch.float32 (default) or torch.bfloat16; taken from ``out`` when that is given."""
     torch = _torch()
     t, k = _matrix(x_q, torch.int8, "x_q")
-    n = _matrix(w_q, torch.int8, "w_q")[0]
+    n = w_q.shape[0] if getattr(w_q, "ndim", 0) == 2 else _matrix(w_q, torch.int8, "w_q")[0]
     dev = x_q.get_device()
     if dtype is None:
         dtype = torch.float32 if out is None else out.dtype
@@ -636,8 +640,7 @@ def i8_matmul(x_q, x_scales, w_q, w_scales, out=None, dtype=None):
         raise TypeError(f"i8_matmul gives torch.float32 or torch.bfloat16, not {dtype}")
     if out is None:
         out = x_q.new_empty((t, n), dtype=dtype)
-    lib = _lib if _lib is not None else _load()
-    _call("stq1_i8_matmul", dev, lib.stq1_i8_matmul, x_q.data_ptr(),
+    _call("stq1_i8_matmul", dev, x_q.data_ptr(),
           _operand(x_scales, torch.float32, (t,), dev, "x_scales"), _operand(w_q, torch.int8, (n, k), dev, "w_q"),
           _operand(w_scales, torch.float32, (n,), dev, "w_scales"), _operand(out, dtype, (t, n), dev, "out"),
           TYPE_F32 if dtype is torch.float32 else TYPE_BF16, t, n, k, _stream(x_q))
@@ -648,18 +651,17 @@ def i8_ffn(x, gateup_q, gateup_scales, down_q, down_scales, out=None, ws=None):
     """Gated feed-forward layer at 8 bits: bf16 x [T, H], int8 gate/up [N, H] and down [H, N/2] -> fp32 [T, H]."""
     torch = _torch()
     t, h = _matrix(x, torch.bfloat16, "x")
-    n = _matrix(gateup_q, torch.int8, "gateup_q")[0]
+    n = gateup_q.shape[0] if getattr(gateup_q, "ndim", 0) == 2 else _matrix(gateup_q, torch.int8, "gateup_q")[0]
     dev = x.get_device()
     if out is None:
         out = torch.empty_like(x, dtype=torch.float32)
-    lib = _lib if _lib is not None else _load()
     args = (x.data_ptr(), _operand(gateup_q, torch.int8, (n, h), dev, "gateup_q"),
             _operand(gateup_scales, torch.float32, (n,), dev, "gateup_scales"),
             _operand(down_q, torch.int8, (h, n // 2), dev, "down_q"),
             _operand(down_scales, torch.float32, (h,), dev, "down_scales"),
             _operand(out, torch.float32, (t, h), dev, "out"))
-    ws = _scratch(ws, lib.stq1_i8_ffn_workspace(t, n, h), x, dev)
-    _call("stq1_i8_ffn", dev, lib.stq1_i8_ffn, *args, t, n, h, ws.data_ptr(), ws.numel(), _stream(x))
+    ws = _scratch(ws, _load().stq1_i8_ffn_workspace(t, n, h) if ws is None else 0, x, dev)
+    _call("stq1_i8_ffn", dev, *args, t, n, h, ws.data_ptr(), ws.numel(), _stream(x))
     return out
 
 
@@ -668,15 +670,14 @@ def glu(x, w, save: bool = False, out=None, y=None):
     up rows).  With ``save`` returns (act, y): y [T, N] bf16 is what glu_backward needs."""
     torch = _torch()
     t, k = _matrix(x, torch.bfloat16, "x")
-    n = _matrix(w, torch.bfloat16, "w")[0]
+    n = w.shape[0] if getattr(w, "ndim", 0) == 2 else _matrix(w, torch.bfloat16, "w")[0]
     dev = x.get_device()
     save = save or y is not None
     if out is None:
         out = x.new_empty((t, n // 2))
     if save and y is None:
         y = x.new_empty((t, n))
-    lib = _lib if _lib is not None else _load()
-    _call("stq1_glu", dev, lib.stq1_glu, x.data_ptr(), _operand(w, torch.bfloat16, (n, k), dev, "w"),
+    _call("stq1_glu", dev, x.data_ptr(), _operand(w, torch.bfloat16, (n, k), dev, "w"),
           _operand(out, torch.bfloat16, (t, n // 2), dev, "out"),
           _operand(y, torch.bfloat16, (t, n), dev, "y") if save else None, t, n, k, _stream(x))
     return (out, y) if save else out
@@ -696,7 +697,6 @@ def glu_backward(dact, y, x, w, dx=None, dw=None, need_dx: bool = True, need_dw:
     # (empty_like is quicker than new_empty)
     dx = None if not need_dx else dx if dx is not None else y.new_empty((t, k)) if x is None else torch.empty_like(x)
     dw = None if not need_dw else dw if dw is not None else y.new_empty((n, k)) if w is None else torch.empty_like(w)
-    lib = _lib if _lib is not None else _load()
     at = lambda v, shape, name: None if v is None else _operand(v, torch.bfloat16, shape, dev, name)  # noqa: E731
     args = (_operand(dact, torch.bfloat16, (t, n // 2), dev, "dact"), y.data_ptr(), at(x, (t, k), "x"),
             at(w, (n, k), "w"), at(dx, (t, k), "dx"), at(dw, (n, k), "dw"))
@@ -706,7 +706,7 @@ def glu_backward(dact, y, x, w, dx=None, dw=None, need_dx: bool = True, need_dw:
     else:
         ws = _scratch(ws, 0, y, dev)
         nbytes = ws.numel()
-    _call("stq1_glu_backward", dev, lib.stq1_glu_backward, *args, t, n, k, ws.data_ptr(), nbytes, _stream(y))
+    _call("stq1_glu_backward", dev, *args, t, n, k, ws.data_ptr(), nbytes, _stream(y))
     return dx, dw
 
 

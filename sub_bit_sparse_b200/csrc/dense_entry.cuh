@@ -36,27 +36,50 @@ bool make_operand_map(CUtensorMap* map, const void* base, bool i8, long long row
 
 std::atomic<bool> g_dense_configured[kMaxDevices];
 constexpr int kFewAllSmem = 232448;
-template <int EPI, bool QX, int MT, int NT>
+template <int EPI, int CODES, int MT, int NT>
 bool few_config_one() {
-  return cudaFuncSetAttribute(dense_few_kernel<EPI, QX, MT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(dense_few_kernel<EPI, CODES, MT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kFewAllSmem) == cudaSuccess;
 }
-template <int EPI, bool QX>
+template <int EPI, int CODES>
 bool few_config() {
-  return few_config_one<EPI, QX, 2, 1>() && few_config_one<EPI, QX, 2, 2>() && few_config_one<EPI, QX, 4, 1>() &&
-         few_config_one<EPI, QX, 4, 2>();
+  return few_config_one<EPI, CODES, 2, 1>() && few_config_one<EPI, CODES, 2, 2>() && few_config_one<EPI, CODES, 4, 1>() &&
+         few_config_one<EPI, CODES, 4, 2>();
 }
-template <int EPI, bool AMN, bool BMN, int S>
+std::atomic<int> g_max_clusters[kMaxDevices][4];   // clusters of 1, 2, 4, 8 CTAs of the split kernel that run at once
+template <int EPI, bool AMN, bool BMN, bool DUAL, int S>
 bool split_config() {
-  return cudaFuncSetAttribute(dense_split_kernel<EPI, AMN, BMN, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(dense_split_kernel<EPI, AMN, BMN, DUAL, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kSplitSmemBytes) == cudaSuccess;
 }
-template <int EPI, bool AMN, bool BMN>
-bool dense_config() {
-  return cudaFuncSetAttribute(dense_pair_kernel<EPI, AMN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int EPI, bool AMN, bool BMN, bool DUAL>
+bool tile_config() {
+  return cudaFuncSetAttribute(dense_pair_kernel<EPI, AMN, BMN, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kPairSmemBytes) == cudaSuccess &&
-         split_config<EPI, AMN, BMN, 1>() && split_config<EPI, AMN, BMN, 2>() && split_config<EPI, AMN, BMN, 4>() &&
-         split_config<EPI, AMN, BMN, 8>();
+         split_config<EPI, AMN, BMN, DUAL, 1>() && split_config<EPI, AMN, BMN, DUAL, 2>() &&
+         split_config<EPI, AMN, BMN, DUAL, 4>() && split_config<EPI, AMN, BMN, DUAL, 8>();
+}
+// How many clusters of S CTAs, one CTA per SM, the device runs at once: clusters
+// stay inside a GPC, so this is less than SMs / S.
+template <int S>
+int query_clusters() {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, S);
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes = kSplitSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = S;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, dense_split_kernel<kEpiI8F32, false, false, false, S>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return n;
 }
 int ensure_dense_configured() {
   const int dev = current_device();
@@ -64,14 +87,20 @@ int ensure_dense_configured() {
   if (g_dense_configured[dev].load(std::memory_order_acquire)) return STQ1_OK;
   std::lock_guard<std::mutex> lock(g_config_mutex);
   if (g_dense_configured[dev].load(std::memory_order_relaxed)) return STQ1_OK;
-  if (!(dense_config<kEpiI8F32, false, false>() && dense_config<kEpiI8Bf16, false, false>() &&
-        dense_config<kEpiI8Glu, false, false>() && dense_config<kEpiGlu, false, false>() &&
-        few_config<kEpiI8F32, false>() && few_config<kEpiI8F32, true>() && few_config<kEpiI8Bf16, false>() &&
-        few_config<kEpiI8Glu, false>() && few_config<kEpiI8Glu, true>() && few_config<kEpiGlu, false>() &&
-        dense_config<kEpiBf16, false, true>() && dense_config<kEpiBf16, true, true>())) {
+  if (!(tile_config<kEpiI8F32, false, false, false>() && tile_config<kEpiI8Bf16, false, false, false>() &&
+        tile_config<kEpiI8Glu, false, false, false>() && tile_config<kEpiGlu, false, false, false>() &&
+        tile_config<kEpiBf16, false, true, false>() && tile_config<kEpiBf16, true, true, false>() &&
+        tile_config<kEpiBf16, false, true, true>() &&
+        few_config<kEpiI8F32, kCodesGiven>() && few_config<kEpiI8F32, kCodesMade>() &&
+        few_config<kEpiI8F32, kCodesMadeKnown>() && few_config<kEpiI8Bf16, kCodesGiven>() &&
+        few_config<kEpiI8Glu, kCodesGiven>() && few_config<kEpiI8Glu, kCodesMade>() && few_config<kEpiGlu, kCodesGiven>())) {
     cudaGetLastError();
     return STQ1_ERR_CUDA;
   }
+  g_max_clusters[dev][0].store(sm_count(), std::memory_order_relaxed);
+  g_max_clusters[dev][1].store(query_clusters<2>(), std::memory_order_relaxed);
+  g_max_clusters[dev][2].store(query_clusters<4>(), std::memory_order_relaxed);
+  g_max_clusters[dev][3].store(query_clusters<8>(), std::memory_order_relaxed);
   g_dense_configured[dev].store(true, std::memory_order_release);
   return STQ1_OK;
 }
@@ -86,54 +115,106 @@ struct DenseProduct {
   uint16_t* y;
 };
 
-template <int EPI, bool AMN, bool BMN>
-int launch_tiles(const DenseProduct& d, cudaStream_t s) {
-  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
-  int rc = ensure_dense_configured();
-  if (rc != STQ1_OK) return rc;
+// One product on the tile kernels, or two (DUAL: d1's A is MN-major) as one launch.
+template <bool I8, bool GLU, bool AMN, bool BMN>
+bool operand_maps(const DenseProduct& d, int box_a, CUtensorMap* ma, CUtensorMap* mb) {
+  const long long rows_b = GLU ? 2 * d.N : d.N;
+  return make_operand_map(ma, d.a, I8, AMN ? d.K : d.M, AMN ? d.M : d.K, box_a) &&
+         make_operand_map(mb, d.b, I8, BMN ? d.K : rows_b, BMN ? rows_b : d.K, 64);
+}
+int k_steps(long long K, bool i8) { return static_cast<int>((K * (i8 ? 1 : 2) + kDnStepBytes - 1) / kDnStepBytes); }
+template <bool I8>
+DenseArgs tile_args(const DenseProduct& d, long long tiles_m, long long tiles_n, int a_rows) {
   DenseArgs p{};
   p.M = d.M;
   p.N = d.N;
-  p.n_k = static_cast<int>((d.K * (I8 ? 1 : 2) + kDnStepBytes - 1) / kDnStepBytes);
+  p.n_k = k_steps(d.K, I8);
+  p.a_bytes = a_rows * kDnStepBytes;
+  p.tiles_m = static_cast<int>(tiles_m);
+  p.tiles_n = static_cast<int>(tiles_n);
   p.sx = d.sx;
   p.sw = d.sw;
   p.out = d.out;
   p.y = d.y;
-  const long long rows_b = GLU ? 2 * d.N : d.N;
-  const int sms = sm_count();
-  // pairs: 256 rows x 256 columns of B; singles: 128 x 128
-  const long long pm = (d.M + 255) / 256, pn = (rows_b + 255) / 256;
-  const long long qm = (d.M + 127) / 128, qn = (rows_b + 127) / 128;
-  const bool pair = qm * qn > sms;
-  CUtensorMap ma, mb;
-  // a lone row of tiles copies no more rows of A than there are (the sums of the others are never stored)
-  const int a_rows = !AMN && !pair && d.M < kDnRows ? static_cast<int>((d.M + 7) / 8 * 8) : kDnRows;
-  p.a_bytes = a_rows * kDnStepBytes;
-  const int box_a = AMN ? 64 : a_rows, box_b = BMN || (GLU && !pair) ? 64 : 128;
-  if (!make_operand_map(&ma, d.a, I8, AMN ? d.K : d.M, AMN ? d.M : d.K, box_a) ||
-      !make_operand_map(&mb, d.b, I8, BMN ? d.K : rows_b, BMN ? rows_b : d.K, box_b))
-    return STQ1_ERR_CUDA;
-  if (pair) {
-    if (pm * pn >= (1LL << 30)) return STQ1_ERR_SHAPE;
-    p.tiles_m = static_cast<int>(pm);
-    p.tiles_n = static_cast<int>(pn);
-    const unsigned grid = 2u * static_cast<unsigned>(std::min<long long>(pm * pn, sms / 2));
-    return launch_pdl(dense_pair_kernel<EPI, AMN, BMN>, grid, kPairThreads, kPairSmemBytes, s, ma, mb, p);
+  return p;
+}
+// 128 x 128 tiles of a product (for the gated forms of 64 outputs)
+template <bool GLU>
+long long single_tiles(const DenseProduct& d) {
+  return (d.M + 127) / 128 * (((GLU ? 2 * d.N : d.N) + 127) / 128);
+}
+
+template <int EPI, bool AMN, bool BMN, bool DUAL>
+int launch_pairs(const DenseProduct& d0, const DenseProduct& d1, cudaStream_t s) {
+  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
+  CUtensorMap a0, b0, a1, b1;
+  if (!operand_maps<I8, GLU, AMN, BMN>(d0, 64, &a0, &b0)) return STQ1_ERR_CUDA;
+  if (DUAL ? !operand_maps<I8, GLU, true, BMN>(d1, 64, &a1, &b1) : (a1 = a0, b1 = b0, false)) return STQ1_ERR_CUDA;
+  const DenseProduct* d[2] = {&d0, &d1};
+  long long tiles[2] = {0, 0};
+  PairArgs args{};
+  for (int i = 0; i < (DUAL ? 2 : 1); ++i) {
+    const long long tm = (d[i]->M + 255) / 256, tn = ((GLU ? 2 * d[i]->N : d[i]->N) + 255) / 256;
+    tiles[i] = tm * tn;
+    if (tiles[i] >= (1LL << 29)) return STQ1_ERR_SHAPE;
+    args.p[i] = tile_args<I8>(*d[i], tm, tn, kDnRows);
   }
-  p.tiles_m = static_cast<int>(qm);
-  p.tiles_n = static_cast<int>(qn);
+  const int clusters = sm_count() / 2;
+  args.tiles0 = static_cast<int>(tiles[0]);
+  args.tiles = static_cast<int>(tiles[0] + tiles[1]);
+  // a last round that would leave more than half of the pairs idle goes by half tiles
+  const int rest = args.tiles % clusters;
+  args.full = 2 * rest <= clusters ? args.tiles - rest : args.tiles;
+  const int units = args.full + 2 * (args.tiles - args.full);
+  return launch_pdl(dense_pair_kernel<EPI, AMN, BMN, DUAL>, 2u * static_cast<unsigned>(std::min(units, clusters)),
+                    kPairThreads, kPairSmemBytes, s, a0, b0, a1, b1, args);
+}
+
+// Pieces of K for so many tiles of n_k steps: as many as run at once, two steps each at least.
+int split_pieces(long long tiles, int n_k) {
+  const int dev = current_device();
   int S = 1;
-  while (2 * S <= kSplitMax && 2 * S <= p.n_k && qm * qn * 2 * S <= sms) S *= 2;
+  for (int i = 1; i <= 3; ++i)
+    if (dev >= 0 && tiles <= g_max_clusters[dev][i].load(std::memory_order_relaxed) && (2 << i) <= n_k) S = 1 << i;
+  return S;
+}
+
+template <int EPI, bool AMN, bool BMN, bool DUAL>
+int launch_split(const DenseProduct& d0, const DenseProduct& d1, int S, cudaStream_t s) {
+  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
+  // a lone row of tiles copies no more rows of A than there are (the sums of the others are never stored)
+  const int a_rows = !AMN && d0.M < kDnRows ? static_cast<int>((d0.M + 7) / 8 * 8) : kDnRows;
+  CUtensorMap a0, b0, a1, b1;
+  if (!operand_maps<I8, GLU, AMN, BMN>(d0, AMN ? 64 : a_rows, &a0, &b0)) return STQ1_ERR_CUDA;
+  if (DUAL ? !operand_maps<I8, GLU, true, BMN>(d1, 64, &a1, &b1) : (a1 = a0, b1 = b0, false)) return STQ1_ERR_CUDA;
+  const DenseProduct* d[2] = {&d0, &d1};
+  long long tiles = 0;
+  SplitArgs args{};
+  for (int i = 0; i < (DUAL ? 2 : 1); ++i) {
+    const long long tm = (d[i]->M + 127) / 128, tn = ((GLU ? 2 * d[i]->N : d[i]->N) + 127) / 128;
+    if (i == 1) args.tiles0 = static_cast<int>(tiles);
+    tiles += tm * tn;
+    args.p[i] = tile_args<I8>(*d[i], tm, tn, i == 0 ? a_rows : kDnRows);
+  }
   auto launch = [&](auto kernel) {
-    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(qm * qn), static_cast<unsigned>(S)), kSplitThreads,
-                              kSplitSmemBytes, s, static_cast<unsigned>(S), ma, mb, p);
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(S)), kSplitThreads,
+                              kSplitSmemBytes, s, static_cast<unsigned>(S), a0, b0, a1, b1, args);
   };
   switch (S) {
-    case 1: return launch(dense_split_kernel<EPI, AMN, BMN, 1>);
-    case 2: return launch(dense_split_kernel<EPI, AMN, BMN, 2>);
-    case 4: return launch(dense_split_kernel<EPI, AMN, BMN, 4>);
-    default: return launch(dense_split_kernel<EPI, AMN, BMN, 8>);
+    case 1: return launch(dense_split_kernel<EPI, AMN, BMN, DUAL, 1>);
+    case 2: return launch(dense_split_kernel<EPI, AMN, BMN, DUAL, 2>);
+    case 4: return launch(dense_split_kernel<EPI, AMN, BMN, DUAL, 4>);
+    default: return launch(dense_split_kernel<EPI, AMN, BMN, DUAL, 8>);
   }
+}
+
+// More 128 x 128 tiles than SMs: pairs on 256 x 256 tiles; else one tile per CTA, K split.
+template <int EPI, bool AMN, bool BMN>
+int launch_tiles(const DenseProduct& d, cudaStream_t s) {
+  int rc = ensure_dense_configured();
+  if (rc != STQ1_OK) return rc;
+  if (single_tiles<epi_glu(EPI)>(d) > sm_count()) return launch_pairs<EPI, AMN, BMN, false>(d, d, s);
+  return launch_split<EPI, AMN, BMN, false>(d, d, split_pieces(single_tiles<epi_glu(EPI)>(d), k_steps(d.K, epi_i8(EPI))), s);
 }
 
 // How a product with few tokens is laid out: outputs per CTA so that every SM
@@ -167,9 +248,10 @@ struct FewChain {
   bool early;
   const void* next;
   long long next_bytes;
+  uint32_t* amax;                    // see FewArgs
 };
 
-template <int EPI, bool QX>
+template <int EPI, int CODES>
 int launch_few(const FewPlan& f, const DenseProduct& d, const FewChain& c, cudaStream_t s) {
   constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
   int rc = ensure_dense_configured();
@@ -188,6 +270,7 @@ int launch_few(const FewPlan& f, const DenseProduct& d, const FewChain& c, cudaS
   p.n_k = f.n_k;
   p.n_slots = f.n_slots;
   p.early = c.early;
+  p.amax = c.amax;
   p.next = static_cast<const char*>(c.next);
   p.next_bytes = c.next_bytes;
   CUtensorMap mw;
@@ -195,8 +278,8 @@ int launch_few(const FewPlan& f, const DenseProduct& d, const FewChain& c, cudaS
   const unsigned grid = static_cast<unsigned>((d.N + f.rows - 1) / f.rows);
   auto launch = [&](auto kernel) { return launch_pdl(kernel, grid, kFewThreads, f.smem, s, mw, p); };
   if (f.pad > 32)
-    return d.M > 8 ? launch(dense_few_kernel<EPI, QX, 4, 2>) : launch(dense_few_kernel<EPI, QX, 4, 1>);
-  return d.M > 8 ? launch(dense_few_kernel<EPI, QX, 2, 2>) : launch(dense_few_kernel<EPI, QX, 2, 1>);
+    return d.M > 8 ? launch(dense_few_kernel<EPI, CODES, 4, 2>) : launch(dense_few_kernel<EPI, CODES, 4, 1>);
+  return d.M > 8 ? launch(dense_few_kernel<EPI, CODES, 2, 2>) : launch(dense_few_kernel<EPI, CODES, 2, 1>);
 }
 
 // A product of K-major operands: few tokens take the streaming kernel.
@@ -204,14 +287,25 @@ template <int EPI>
 int launch_product(const DenseProduct& d, cudaStream_t s) {
   FewPlan f;
   if (plan_few(&f, d.M, d.N, d.K * (epi_i8(EPI) ? 1 : 2), epi_glu(EPI)))
-    return launch_few<EPI, false>(f, d, FewChain{}, s);
+    return launch_few<EPI, kCodesGiven>(f, d, FewChain{}, s);
   return launch_tiles<EPI, false, false>(d, s);
 }
 
-int launch_quant_i8(const void* src, int type, long long R, long long K, int8_t* q, float* scales, cudaStream_t s) {
-  if (type == STQ1_TYPE_F32)
-    return launch_pdl(quant_i8_kernel<true>, static_cast<unsigned>(R), kQi8Threads, 0, s, src, K, q, scales);
-  return launch_pdl(quant_i8_kernel<false>, static_cast<unsigned>(R), kQi8Threads, 0, s, src, K, q, scales);
+// Rows of up to 2048 values take a warp each (from 1024 on with eight vectors in flight per lane), longer ones a CTA.
+template <bool F32>
+int launch_quant_rows(const void* src, long long R, long long K, int8_t* q, float* scales, uint32_t* clear,
+                      cudaStream_t s) {
+  constexpr int kPer = kQi8Threads / 32;
+  const unsigned warps = static_cast<unsigned>((R + kPer - 1) / kPer);
+  if (K <= 1024) return launch_pdl(quant_i8_kernel<F32, 32, 4>, warps, kQi8Threads, 0, s, src, R, K, q, scales, clear);
+  if (K <= 2048) return launch_pdl(quant_i8_kernel<F32, 32, 8>, warps, kQi8Threads, 0, s, src, R, K, q, scales, clear);
+  return launch_pdl(quant_i8_kernel<F32, kQi8Threads, 4>, static_cast<unsigned>(R), kQi8Threads, 0, s, src, R, K, q,
+                    scales, clear);
+}
+int launch_quant_i8(const void* src, int type, long long R, long long K, int8_t* q, float* scales, cudaStream_t s,
+                    uint32_t* clear = nullptr) {
+  return type == STQ1_TYPE_F32 ? launch_quant_rows<true>(src, R, K, q, scales, clear, s)
+                               : launch_quant_rows<false>(src, R, K, q, scales, clear, s);
 }
 
 DenseProduct i8_product(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, void* out, long long T,
@@ -297,13 +391,26 @@ extern "C" int stq1_glu_backward(const uint16_t* dact, const uint16_t* y, const 
   int rc = launch_pdl(glu_dy_kernel, static_cast<unsigned>(grid), 256, 0, s, dact, y, dy, static_cast<long long>(T),
                       static_cast<long long>(N / 2));
   if (rc != STQ1_OK) return rc;
-  if (dx) {                              // dX[t, k] = sum_n dY[t, n] W[n, k]
-    rc = launch_tiles<kEpiBf16, false, true>({dy, W, T, K, N, nullptr, nullptr, dx, nullptr}, s);
+  const DenseProduct px{dy, W, T, K, N, nullptr, nullptr, dx, nullptr};    // dX[t, k] = sum_n dY[t, n] W[n, k]
+  const DenseProduct pw{dy, x, N, K, T, nullptr, nullptr, dW, nullptr};    // dW[n, k] = sum_t dY[t, n] x[t, k]
+  rc = ensure_dense_configured();
+  if (rc != STQ1_OK) return rc;
+  // one launch for both where the same kernel suits both; a gradient has the
+  // same bits whether the other is asked for or not, so few tiles are split
+  // as for both in any case
+  const long long tx = single_tiles<false>(px), tw = single_tiles<false>(pw);
+  if (tx + tw <= sm_count()) {
+    const int S = split_pieces(tx + tw, std::max(k_steps(N, false), k_steps(T, false)));
+    if (dx && dW) return launch_split<kEpiBf16, false, true, true>(px, pw, S, s);
+    return dx ? launch_split<kEpiBf16, false, true, false>(px, px, S, s)
+              : launch_split<kEpiBf16, true, true, false>(pw, pw, S, s);
+  }
+  if (dx && dW && tx > sm_count() && tw > sm_count()) return launch_pairs<kEpiBf16, false, true, true>(px, pw, s);
+  if (dx) {
+    rc = launch_tiles<kEpiBf16, false, true>(px, s);
     if (rc != STQ1_OK) return rc;
   }
-  if (dW)                                // dW[n, k] = sum_t dY[t, n] x[t, k]
-    rc = launch_tiles<kEpiBf16, true, true>({dy, x, N, K, T, nullptr, nullptr, dW, nullptr}, s);
-  return rc;
+  return dW ? launch_tiles<kEpiBf16, true, true>(pw, s) : rc;
 }
 
 extern "C" size_t stq1_i8_ffn_workspace(int64_t T, int64_t N, int64_t H) {
@@ -334,19 +441,21 @@ extern "C" int stq1_i8_ffn(const uint16_t* x, const int8_t* gateup_q, const floa
   if (plan_few(&fg, T, N / 2, H, true) && plan_few(&fd, T, H, N / 2, false)) {
     // few tokens: each kernel streams its weights while the one before it
     // still runs, and the first brings the second's into L2
-    const FewChain c1{false, down_q, static_cast<long long>(H) * (N / 2)}, c2{true, nullptr, 0};
+    const long long next_bytes = static_cast<long long>(H) * (N / 2);
+    DenseProduct dn = down;
+    dn.a = act;
     int rc;
-    if (T <= kFfnFusedTokens) {           // codes made inside the products: two launches
-      DenseProduct u = up, dn = down;
+    if (T <= kFfnFusedTokens) {           // codes made inside both products: two launches
+      DenseProduct u = up;
       u.a = x;
-      dn.a = act;
-      rc = launch_few<kEpiI8Glu, true>(fg, u, c1, s);
-      return rc != STQ1_OK ? rc : launch_few<kEpiI8F32, true>(fd, dn, c2, s);
+      rc = launch_few<kEpiI8Glu, kCodesMade>(fg, u, FewChain{false, down_q, next_bytes, nullptr}, s);
+      return rc != STQ1_OK ? rc : launch_few<kEpiI8F32, kCodesMade>(fd, dn, FewChain{true, nullptr, 0, nullptr}, s);
     }
-    rc = launch_quant_i8(x, STQ1_TYPE_BF16, T, H, xq, sx, s);
-    if (rc == STQ1_OK) rc = launch_few<kEpiI8Glu, false>(fg, up, FewChain{true, c1.next, c1.next_bytes}, s);
-    if (rc == STQ1_OK) rc = launch_quant_i8(act, STQ1_TYPE_BF16, T, N / 2, aq, sa, s);
-    return rc != STQ1_OK ? rc : launch_few<kEpiI8F32, false>(fd, down, c2, s);
+    // the activation's maxima are kept by the kernel that writes it
+    uint32_t* amax = reinterpret_cast<uint32_t*>(sa);
+    rc = launch_quant_i8(x, STQ1_TYPE_BF16, T, H, xq, sx, s, amax);
+    if (rc == STQ1_OK) rc = launch_few<kEpiI8Glu, kCodesGiven>(fg, up, FewChain{true, down_q, next_bytes, amax}, s);
+    return rc != STQ1_OK ? rc : launch_few<kEpiI8F32, kCodesMadeKnown>(fd, dn, FewChain{true, nullptr, 0, amax}, s);
   }
   int rc = launch_quant_i8(x, STQ1_TYPE_BF16, T, H, xq, sx, s);
   if (rc != STQ1_OK) return rc;

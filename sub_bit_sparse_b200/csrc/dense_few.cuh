@@ -46,6 +46,8 @@ struct FewArgs {
   int n_k;                     // 128-byte steps of K
   int n_slots;
   int early;                   // the weights are not written by the kernel before: load them at once
+  uint32_t* amax;              // fp32 bits of each token's largest magnitude: of x, read (kCodesMadeKnown);
+                               // of the gated output, raised (8-bit gated form), or NULL
   const char* next;            // weights of the kernel after, brought into L2 at the end, or NULL
   long long next_bytes;
 };
@@ -67,13 +69,17 @@ __device__ __forceinline__ void few_mma(float (&c)[4], uint32_t a0, uint32_t a1,
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// QX: x is bf16 and its codes are made here: each CTA finds the tokens' scales
-// itself, T * K values from L2, while its first weights are on their way.
+// Where the tokens' codes come from: they are given; or x is bf16 and they are
+// made here, from each token's largest magnitude, which each CTA finds for
+// itself (T * K values from L2, while its first weights are on their way) or
+// reads (the kernel that wrote x kept it).
+enum FewCodes { kCodesGiven, kCodesMade, kCodesMadeKnown };
+
 // MT: fragments of 16 weight rows (at most); NT: groups of 8 tokens.
-template <int EPI, bool QX, int MT, int NT>
+template <int EPI, int CODES, int MT, int NT>
 __global__ void __launch_bounds__(kFewThreads, 2)
 dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
-  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
+  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI), QX = CODES != kCodesGiven;
   static_assert(I8 || !QX, "codes are made for 8-bit weights");
   using Acc = std::conditional_t<I8, int, float>;
   constexpr int ES = I8 ? 1 : 2;
@@ -100,6 +106,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
     dn_load<1>(dst, &map_w, step * kStep, y0, bar);
     if constexpr (GLU) dn_load<1>(dst + slot_bytes / 2, &map_w, step * kStep, y1, bar);
   };
+  if (threadIdx.x == 0) dn_prefetch_map(&map_w);
   if (lane == 0) {
     for (int i = 0; i < p.n_slots; ++i) mbar_init(my_bar + 8 * i, 1);
     if (warp == 0) mbar_init(bar_x, 1);
@@ -138,7 +145,9 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
       const int tok = tok0 + warp / per;
       const char* xr = static_cast<const char*>(p.x) + tok * p.K * 2;
       uint32_t m = 0u;
-      if (tok < p.T) {
+      if (CODES == kCodesMadeKnown) {
+        m = tok < p.T ? __ldcg(p.amax + tok) : 0u;
+      } else if (tok < p.T) {
 #pragma unroll 4
         for (int i = first; i < nv; i += 32 * per) {
           Row8<false> a, b;
@@ -147,8 +156,8 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
           m = max(m, max(a.amax_bits(), b.amax_bits()));
         }
       }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (per > 1) {
+      if (CODES == kCodesMade) m = __reduce_max_sync(0xffffffffu, m);
+      if (CODES == kCodesMade && per > 1) {
         if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(s_max + 4 * warp), "r"(m) : "memory");
         __syncthreads();
         for (int i = 0; i < per; ++i) {
@@ -247,6 +256,9 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
                    "r"(*reinterpret_cast<const uint32_t*>(&acc[i][n][0])), "r"(*reinterpret_cast<const uint32_t*>(&acc[i][n][1])),
                    "r"(*reinterpret_cast<const uint32_t*>(&acc[i][n][2])), "r"(*reinterpret_cast<const uint32_t*>(&acc[i][n][3]))
                    : "memory");
+  // the CTA's largest outputs of each token (8-bit gated form)
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem_raw + (bar_x + 8 - sraw));
+  if (EPI == kEpiI8Glu && threadIdx.x < kFewMaxTokens) s_amax[threadIdx.x] = 0u;
   if (__syncthreads_or(!ok)) return;                 // a wait ran out (flagged): nothing is stored
 
   // sums over the warps, in their order; consecutive threads take consecutive outputs of one token
@@ -277,7 +289,10 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
     };
     if constexpr (GLU) {
       const float gv = value(total(0), n), uv = value(total(2), p.N + n);
-      static_cast<uint16_t*>(p.out)[tok * p.N + n] = static_cast<uint16_t>(swiglu_bf16(gv, uv));
+      const uint32_t bits = swiglu_bf16(gv, uv);
+      static_cast<uint16_t*>(p.out)[tok * p.N + n] = static_cast<uint16_t>(bits);
+      if constexpr (EPI == kEpiI8Glu)
+        if (p.amax) atomicMax(s_amax + tok, (bits & 0x7FFFu) << 16);
       if constexpr (EPI == kEpiGlu)
         if (p.y) {
           p.y[tok * 2 * p.N + n] = static_cast<uint16_t>(bf16_bits_rn(gv));
@@ -287,6 +302,14 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
       const float v = value(total((r & 8) ? 2 : 0), n);
       if constexpr (EPI == kEpiI8F32) static_cast<float*>(p.out)[tok * p.N + n] = v;
       else static_cast<uint16_t*>(p.out)[tok * p.N + n] = static_cast<uint16_t>(bf16_bits_rn(v));
+    }
+  }
+  if constexpr (EPI == kEpiI8Glu) {
+    // one update per token and CTA: one per output took 9 us at 16 tokens.  (A
+    // maximum does not depend on the order of its updates.)
+    if (p.amax) {
+      __syncthreads();
+      if (threadIdx.x < p.T) atomicMax(p.amax + threadIdx.x, s_amax[threadIdx.x]);
     }
   }
 }

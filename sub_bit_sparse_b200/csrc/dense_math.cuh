@@ -107,6 +107,8 @@ __device__ __forceinline__ bool swiglu_bf16_fast(float g, float u, uint32_t& bit
 }
 __device__ __noinline__ uint32_t swiglu_bf16_slow(float g, float u) {
   const float s = __fdividef(g, 1.f + expf(-g)), v = s * u;
+  // a zero gate or up, as a padded batch has whole rows of (0 * Inf is NaN and goes on)
+  if (v == 0.f && (g == 0.f || u == 0.f)) return __float_as_uint(v) >> 16;
   if (fabsf(s) > 1e-30f && fabsf(v) > 1e-30f && fabsf(v) < 1e38f) return swiglu_bf16_border(g, u);
   return swiglu_bf16_ends(g, u);
 }

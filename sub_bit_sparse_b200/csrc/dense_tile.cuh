@@ -36,6 +36,14 @@ struct DenseArgs {
   uint16_t* y;                       // kEpiGlu: [M, 2N] or NULL
 };
 
+// What the pair kernel works through: one product, or two with the same
+// epilogue that run as one (the second follows the first tile by tile).
+struct PairArgs {
+  DenseArgs p[2];
+  int tiles0, tiles;                 // 256 x 256 tiles of the first product, of both
+  int full;                          // tiles done whole; the others as two halves of 128 columns
+};
+
 constexpr int kDnStepBytes = 128;    // bytes of K per step and row: one swizzle atom
 constexpr int kDnRows = 128;         // rows of A and rows of B per CTA and step
 constexpr int kDnOperandBytes = kDnRows * kDnStepBytes;
@@ -145,17 +153,20 @@ constexpr uint32_t dn_idesc(int m, int n) {
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// One step of an operand into shared memory: 128 rows (K-major) or 128
-// columns (MN-major, two boxes of 64) of 128 bytes of K.
+// One step of an operand into shared memory: rows (K-major) or columns
+// (MN-major) of 128 bytes of K, in `boxes` boxes of 64.
 template <bool I8, bool MN, int CG>
-__device__ __forceinline__ void dn_load_operand(uint32_t dst, const CUtensorMap* map, int step, int row, uint32_t bar) {
+__device__ __forceinline__ void dn_load_operand(uint32_t dst, const CUtensorMap* map, int step, int row, int boxes,
+                                                uint32_t bar) {
   constexpr int kStep = I8 ? 128 : 64;      // values of K per step
-  if constexpr (MN) {
-    dn_load<CG>(dst, map, row, step * kStep, bar);
-    dn_load<CG>(dst + kDnOperandBytes / 2, map, row + 64, step * kStep, bar);
-  } else {
-    dn_load<CG>(dst, map, step * kStep, row, bar);
+  for (int i = 0; i < boxes; ++i) {
+    if constexpr (MN) dn_load<CG>(dst + i * (kDnOperandBytes / 2), map, row + 64 * i, step * kStep, bar);
+    else dn_load<CG>(dst + i * (kDnOperandBytes / 2), map, step * kStep, row + 64 * i, bar);
   }
+}
+
+__device__ __forceinline__ void dn_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 template <bool I8>
@@ -179,36 +190,48 @@ __device__ __forceinline__ void dn_tile_pos(const DenseArgs& p, int tile, int& t
 // Large products: pairs of CTAs on 256 x 256 tiles.
 // ---------------------------------------------------------------------------
 
+// (Five stages measure the same as six, four are 5-9% slower; sixteen epilogue
+// warps with five stages the same for bf16 results and 5% slower for fp32.)
 constexpr int kPairStages = 6;
-constexpr int kPairThreads = 320;                   // warps 0-7 epilogue, 8 producer, 9 MMA
+constexpr int kPairEpi = 8;                         // epilogue warps: TMEM quadrants x column blocks in turn
+constexpr int kPairSides = kPairEpi / 4;
+constexpr int kPairWarpA = kPairEpi, kPairWarpMma = kPairEpi + 1, kPairWarpB = kPairEpi + 2;
+constexpr int kPairThreads = 32 * (kPairEpi + 3);
 constexpr int kPairOffStage = kPairStages * kDnStageBytes;
-constexpr int kPairOffBar = kPairOffStage + 8 * 4096;
+constexpr int kPairOffBar = kPairOffStage + kPairEpi * 4096;
 constexpr int kPairSmemBytes = 1024 + kPairOffBar + 256;
 static_assert(kPairSmemBytes <= 232448, "shared memory per CTA is at most 227 KB");
 
-// One warp's 32 x 32 words (row = lane) to global memory through 4 KB of
-// shared memory: 16-byte pieces at piece ^ (row & 7), so that neither the
-// row-wise stores nor the reads of whole rows meet on a bank; then eight lanes
-// store 128 bytes of one row.  ES: bytes of an element; a word holds 4 / ES.
-template <int ES>
-__device__ __forceinline__ void dn_store_block(const uint32_t (&w)[32], uint32_t buf, void* out, long long row0,
+// One warp's 32 rows of WORDS words (row = lane) to global memory through
+// shared memory: 16-byte pieces at piece ^ (row & 7) (of four pieces, & 3),
+// so that neither the row-wise stores nor the reads of whole rows meet on a
+// bank; then WORDS / 4 lanes store a row's piece each.  ES: bytes of an
+// element; a word holds 4 / ES.
+template <int ES, int WORDS>
+__device__ __forceinline__ void dn_store_block(const uint32_t* w, uint32_t buf, void* out, long long row0,
                                                long long rows, long long ld, long long col0, long long cols, bool vec) {
   const int lane = threadIdx.x & 31;
   constexpr int kPer = 4 / ES;                      // elements per word
+  constexpr int kPieces = WORDS / 4, kPitch = WORDS * 4, kRows = 32 / kPieces;
+  // with four pieces two rows share 128 bytes: rows r and r + 1 keep apart by
+  // themselves, rows r and r + 2 by the swizzle
+  auto place = [](int row, int piece) {
+    return row * kPitch + ((piece ^ (kPieces == 8 ? row & 7 : (row >> 1) & 3)) << 4);
+  };
   __syncwarp();                                     // the previous block's reads are done
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(buf + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(w[4 * c]),
-                 "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+  for (int c = 0; c < kPieces; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(buf + place(lane, c)), "r"(w[4 * c]), "r"(w[4 * c + 1]),
+                 "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
                  : "memory");
   __syncwarp();
   char* base = static_cast<char*>(out);
-  const int piece = lane & 7;
+  const int piece = lane % kPieces;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 4 * i + (lane >> 3);
+  for (int i = 0; i < kPieces; ++i) {
+    const int r = kRows * i + lane / kPieces;
     if (row0 + r >= rows) continue;
-    const uint4 v = lds_v4(buf + r * 128 + ((piece ^ (r & 7)) << 4));
+    const uint4 v = lds_v4(buf + place(r, piece));
     const long long c = col0 + piece * 4 * kPer;
     char* dst = base + ((row0 + r) * ld + c) * ES;
     if (vec) {
@@ -225,10 +248,75 @@ __device__ __forceinline__ void dn_store_block(const uint32_t (&w)[32], uint32_t
   }
 }
 
-template <int EPI, bool AMN, bool BMN>
+// A unit of the pair kernel's work: which product, the tile's place, and
+// whether it is a whole tile or one half of its columns.
+struct PairUnit {
+  int prob, tm, tn, half;            // half: -1 whole, 0 / 1 the left / right 128 columns
+};
+template <bool DUAL>
+__device__ __forceinline__ PairUnit pair_unit(const PairArgs& a, int unit) {
+  PairUnit u;
+  int tile = unit;
+  u.half = -1;
+  if (unit >= a.full) {
+    tile = a.full + ((unit - a.full) >> 1);
+    u.half = (unit - a.full) & 1;
+  }
+  u.prob = DUAL && tile >= a.tiles0 ? 1 : 0;
+  dn_tile_pos(a.p[u.prob], u.prob ? tile - a.tiles0 : tile, u.tm, u.tn);
+  return u;
+}
+
+// A place in the ring of stages: its index and the parity of its use.
+struct RingPos {
+  uint32_t s = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == kPairStages) s = 0, ph ^= 1;
+  }
+};
+
+// The MMAs of one unit: this thread waits for each step's operands (both
+// CTAs'), issues four MMAs and hands the stage back.
+template <bool I8, bool AMN, bool BMN>
+__device__ __forceinline__ bool pair_mmas(uint32_t d, int n_k, uint32_t idesc, uint32_t sbase, uint32_t bar_full,
+                                          uint32_t bar_empty, RingPos& r) {
+  const uint64_t da0 = dn_desc<AMN>(sbase), db0 = dn_desc<BMN>(sbase + kDnOperandBytes);
+  uint32_t acc = 0;
+  for (int k = 0; k < n_k; ++k) {
+    if (!dn_wait_cluster(bar_full + 8 * r.s, r.ph)) return false;
+    tc_fence_after();
+    const uint64_t da = da0 + r.s * (kDnStageBytes >> 4), db = db0 + r.s * (kDnStageBytes >> 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      dn_mma<I8, 2>(d, da + j * dn_advance<AMN>(), db + j * dn_advance<BMN>(), idesc, acc);
+      acc = 1;
+    }
+    dn_commit_pair(bar_empty + 8 * r.s);
+    r.next();
+  }
+  return true;
+}
+
+// This CTA's share of one operand for the steps of one unit.
+template <bool I8, bool MN>
+__device__ __forceinline__ bool pair_loads(const CUtensorMap* map, int n_k, int row, int boxes, uint32_t dst0,
+                                           uint32_t bar_empty, uint32_t bar_full, uint32_t full0, uint32_t expect,
+                                           RingPos& r) {
+  for (int k = 0; k < n_k; ++k) {
+    if (!mbar_wait_bounded(bar_empty + 8 * r.s, r.ph ^ 1)) return false;
+    if (expect) mbar_arrive_expect_tx(bar_full + 8 * r.s, expect);
+    dn_load_operand<I8, MN, 2>(dst0 + r.s * kDnStageBytes, map, k, row, boxes, full0 + 8 * r.s);
+    r.next();
+  }
+  return true;
+}
+
+// DUAL: the second product's A is MN-major (dW beside dX).
+template <int EPI, bool AMN, bool BMN, bool DUAL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                  const DenseArgs p) {
+                  const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b1,
+                  const __grid_constant__ PairArgs args) {
   constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
   static_assert(!(I8 && (AMN || BMN)), "8-bit operands are K-major");
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -241,17 +329,19 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairStages; ++i) {
-      mbar_init(bar_full + 8 * i, 1);
+      mbar_init(bar_full + 8 * i, 2);                // the leader's two producers
       mbar_init(bar_empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_acc_full + 8 * i, 1);
-      mbar_init(bar_acc_empty + 8 * i, 16);          // the epilogue warps of both CTAs
+      mbar_init(bar_acc_empty + 8 * i, 2 * kPairEpi);   // the epilogue warps of both CTAs
     }
     mbar_init(bar_drain, 1);
     fence_mbar_init();
   }
-  if (warp == 9) dn_tmem_alloc<2>(s_tmem, 512);
+  if (warp == kPairWarpMma) dn_tmem_alloc<2>(s_tmem, 512);
+  if (threadIdx.x == 32 * kPairWarpA) dn_prefetch_map(&map_a);
+  if (threadIdx.x == 32 * kPairWarpB) dn_prefetch_map(&map_b);
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -260,54 +350,59 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   griddep_wait();
   griddep_launch_dependents();
 
-  const int n_tiles = p.tiles_m * p.tiles_n;
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int n_units = args.full + 2 * (args.tiles - args.full);
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
-  if (warp == 8) {
-    // ---- producer: this CTA's 128 rows of A and 128 rows of B per step ----
+  if (warp == kPairWarpA || warp == kPairWarpB) {
+    // ---- producers: this CTA's 128 rows of A and 128 or 64 rows of B per step ----
     // A wait that runs out ends the role; it started after the last copy was
     // issued, so no copy is in flight any more by then.
     if (lane == 0) {
       const uint32_t full0 = dn_mapa(bar_full, 0);
-      uint32_t it = 0;
+      RingPos r;
       bool ok = true;
-      for (int tile = first; tile < n_tiles && ok; tile += step) {
-        int tm, tn;
-        dn_tile_pos(p, tile, tm, tn);
-        const int row_a = tm * 256 + static_cast<int>(rank) * kDnRows;
-        // gated: the leader loads the gate rows, its peer the up rows of the same outputs
-        const int row_b = GLU ? static_cast<int>(rank * p.N) + tn * kDnRows : tn * 256 + static_cast<int>(rank) * kDnRows;
-        for (int k = 0; k < p.n_k; ++k, ++it) {
-          const uint32_t s = it % kPairStages, use = it / kPairStages;
-          if (!mbar_wait_bounded(bar_empty + 8 * s, (use & 1) ^ 1)) { ok = false; break; }
-          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, 2 * kDnStageBytes);
-          const uint32_t dst = sbase + s * kDnStageBytes;
-          dn_load_operand<I8, AMN, 2>(dst, &map_a, k, row_a, full0 + 8 * s);
-          dn_load_operand<I8, BMN, 2>(dst + kDnOperandBytes, &map_b, k, row_b, full0 + 8 * s);
+      for (int unit = first; unit < n_units && ok; unit += stride) {
+        const PairUnit u = pair_unit<DUAL>(args, unit);
+        const DenseArgs& p = args.p[u.prob];
+        const int boxes = warp == kPairWarpA || u.half < 0 ? 2 : 1;
+        const uint32_t expect = rank == 0 ? boxes * kDnOperandBytes : 0;      // of both CTAs
+        if (warp == kPairWarpA) {
+          const int row = u.tm * 256 + static_cast<int>(rank) * kDnRows;
+          if (DUAL && u.prob)
+            ok = pair_loads<I8, true>(&map_a1, p.n_k, row, 2, sbase, bar_empty, bar_full, full0, expect, r);
+          else
+            ok = pair_loads<I8, AMN>(&map_a, p.n_k, row, 2, sbase, bar_empty, bar_full, full0, expect, r);
+        } else {
+          // gated: the leader loads the gate rows, its peer the up rows of the same outputs
+          const int half = u.half > 0 ? 1 : 0;
+          const int row = GLU ? static_cast<int>(rank * p.N) + u.tn * 128 + 64 * half
+                              : u.tn * 256 + 128 * half + static_cast<int>(rank) * 64 * boxes;
+          if (DUAL && u.prob)
+            ok = pair_loads<I8, BMN>(&map_b1, p.n_k, row, boxes, sbase + kDnOperandBytes, bar_empty, bar_full, full0,
+                                     expect, r);
+          else
+            ok = pair_loads<I8, BMN>(&map_b, p.n_k, row, boxes, sbase + kDnOperandBytes, bar_empty, bar_full, full0,
+                                     expect, r);
         }
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kPairWarpMma) {
     // ---- MMA issuer (leader only): both CTAs' operands, both CTAs' TMEM ----
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = dn_idesc<I8, AMN, BMN>(256, 256);
-      uint32_t it = 0, t = 0;
+      RingPos r;
+      uint32_t t = 0;
       bool ok = true;
-      for (int tile = first; tile < n_tiles && ok; tile += step, ++t) {
+      for (int unit = first; unit < n_units && ok; unit += stride, ++t) {
         const uint32_t buf = t & 1, use = t >> 1;
         if (!dn_wait_cluster(bar_acc_empty + 8 * buf, (use & 1) ^ 1)) break;
         tc_fence_after();
-        for (int k = 0; k < p.n_k; ++k, ++it) {
-          const uint32_t s = it % kPairStages, ph = (it / kPairStages) & 1;
-          if (!dn_wait_cluster(bar_full + 8 * s, ph)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t da = dn_desc<AMN>(sbase + s * kDnStageBytes);
-          const uint64_t db = dn_desc<BMN>(sbase + s * kDnStageBytes + kDnOperandBytes);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            dn_mma<I8, 2>(tmem + 256 * buf, da + j * dn_advance<AMN>(), db + j * dn_advance<BMN>(), idesc, (k | j) != 0);
-          dn_commit_pair(bar_empty + 8 * s);
-        }
+        const PairUnit u = pair_unit<DUAL>(args, unit);
+        const int n_k = args.p[u.prob].n_k, n = u.half < 0 ? 256 : 128;
+        const uint32_t d = tmem + 256 * buf;
+        if (DUAL && u.prob)
+          ok = pair_mmas<I8, true, BMN>(d, n_k, dn_idesc<I8, true, BMN>(256, n), sbase, bar_full, bar_empty, r);
+        else
+          ok = pair_mmas<I8, AMN, BMN>(d, n_k, dn_idesc<I8, AMN, BMN>(256, n), sbase, bar_full, bar_empty, r);
         dn_commit_pair(bar_acc_full + 8 * buf);
       }
       if (!ok) {
@@ -318,19 +413,19 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       }
     }
   } else {
-    // ---- epilogue: warp w reads TMEM lanes 32 (w & 3).. and half of the columns ----
-    const int quad = warp & 3, half = warp >> 2;
+    // ---- epilogue: warp w reads TMEM lanes 32 (w & 3).. and every kPairSides-th block of columns ----
+    const int quad = warp & 3, side = warp >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
     const uint32_t buf_s = sbase + kPairOffStage + warp * 4096;
     const uint32_t acc_empty0 = dn_mapa(bar_acc_empty, 0);
     constexpr int ES = EPI == kEpiI8F32 ? 4 : 2;
-    const bool vec = p.N % (16 / ES) == 0;
     uint32_t t = 0;
-    for (int tile = first; tile < n_tiles; tile += step, ++t) {
+    for (int unit = first; unit < n_units; unit += stride, ++t) {
       const uint32_t buf = t & 1, use = t >> 1;
-      int tm, tn;
-      dn_tile_pos(p, tile, tm, tn);
-      const long long row0 = tm * 256LL + rank * kDnRows + 32 * quad;
+      const PairUnit un = pair_unit<DUAL>(args, unit);
+      const DenseArgs& p = args.p[un.prob];
+      const bool vec = p.N % (16 / ES) == 0;
+      const long long row0 = un.tm * 256LL + rank * kDnRows + 32 * quad;
       const float sx = I8 && row0 + lane < p.M ? p.sx[row0 + lane] : 0.f;
       if (!mbar_wait_bounded(bar_acc_full + 8 * buf, use & 1)) break;
       tc_fence_after();
@@ -339,77 +434,84 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       auto col_scale = [&](long long first_row, long long col0) {
         return I8 && col0 + lane < p.N ? p.sw[first_row + col0 + lane] : 0.f;
       };
-      if constexpr (GLU) {
-        // act columns [64 half, 64 half + 64) of the tile: gate sums at those columns, up sums 128 further
-        const long long col0 = tn * 128LL + 64 * half;
-        uint32_t act[32], kg[32], ku[32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t g[16], u[16];
-          STQ1_TMEM_LD16(acc + 64 * half + 16 * c, g);
-          STQ1_TMEM_LD16(acc + 128 + 64 * half + 16 * c, u);
-          float swg = 0.f, swu = 0.f;
-          if constexpr (I8) {
-            swg = col_scale(0, col0 + 16 * c);
-            swu = col_scale(p.N, col0 + 16 * c);
-          }
-          tmem_wait_ld();
-          float gv[16], uv[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            gv[i] = dn_sum<I8>(g[i], sx, I8 ? __shfl_sync(0xffffffffu, swg, i) : 0.f);
-            uv[i] = dn_sum<I8>(u[i], sx, I8 ? __shfl_sync(0xffffffffu, swu, i) : 0.f);
-          }
-          swiglu_bf16_pack<16>(gv, uv, act + 8 * c);
-          if constexpr (EPI == kEpiGlu) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              kg[8 * c + i / 2] = bf16_bits_rn(gv[i]) | (bf16_bits_rn(gv[i + 1]) << 16);
-              ku[8 * c + i / 2] = bf16_bits_rn(uv[i]) | (bf16_bits_rn(uv[i + 1]) << 16);
-            }
-          }
-        }
+      auto release = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) dn_arrive_remote(acc_empty0 + 8 * buf);
-        dn_store_block<2>(act, buf_s, p.out, row0, p.M, p.N, col0, p.N, vec);
-        if constexpr (EPI == kEpiGlu)
-          if (p.y) {
-            dn_store_block<2>(kg, buf_s, p.y, row0, p.M, 2 * p.N, col0, p.N, vec);
-            dn_store_block<2>(ku, buf_s, p.y + p.N, row0, p.M, 2 * p.N, col0, p.N, vec);
-          }
-      } else {
-        constexpr int kCols = 128 / ES;              // columns of one 128-byte block of a row
+      };
+      // blocks of 64 columns of B: four of a whole tile, two of a half
+      const int blocks = un.half < 0 ? 4 : 2;
 #pragma unroll 1
-        for (int c = 0; c < 128 / kCols; ++c) {
-          const int tc = 128 * half + kCols * c;
-          const long long col0 = tn * 256LL + tc;
-          uint32_t w[32];
+      for (int blk = side; blk < blocks; blk += kPairSides) {
+        const bool last = blk + kPairSides >= blocks;
+        if constexpr (GLU) {
+          // 32 outputs: gate sums in columns from c0, up sums `up` further
+          const int c0 = 32 * blk, up = un.half < 0 ? 128 : 64;
+          const long long col0 = un.tn * 128LL + c0 + (un.half > 0 ? 64 : 0);
+          float swg = 0.f, swu = 0.f;
+          if constexpr (I8) {
+            swg = col_scale(0, col0);
+            swu = col_scale(p.N, col0);
+          }
+          uint32_t gs[32], us[32];
+          STQ1_TMEM_LD32(acc + c0, gs);
+          STQ1_TMEM_LD32(acc + up + c0, us);
+          tmem_wait_ld();
+          if (last) release();
+          uint32_t act[16], kg[16], ku[16];
 #pragma unroll
-          for (int q = 0; q < kCols / 32; ++q) {
-            uint32_t v[32];
-            STQ1_TMEM_LD32(acc + tc + 32 * q, v);
-            const float sw = col_scale(0, col0 + 32 * q);
-            tmem_wait_ld();
+          for (int c = 0; c < 2; ++c) {
+            float gv[16], uv[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float f[2];
+            for (int i = 0; i < 16; ++i) {
+              gv[i] = dn_sum<I8>(gs[16 * c + i], sx, I8 ? __shfl_sync(0xffffffffu, swg, 16 * c + i) : 0.f);
+              uv[i] = dn_sum<I8>(us[16 * c + i], sx, I8 ? __shfl_sync(0xffffffffu, swu, 16 * c + i) : 0.f);
+            }
+            swiglu_bf16_pack<16>(gv, uv, act + 8 * c);
+            if constexpr (EPI == kEpiGlu) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) f[h] = dn_sum<I8>(v[i + h], sx, I8 ? __shfl_sync(0xffffffffu, sw, i + h) : 0.f);
-              if constexpr (ES == 4) {
-                w[i] = __float_as_uint(f[0]);
-                w[i + 1] = __float_as_uint(f[1]);
-              } else {
-                w[16 * q + i / 2] = bf16_bits_rn(f[0]) | (bf16_bits_rn(f[1]) << 16);
+              for (int i = 0; i < 16; i += 2) {
+                kg[8 * c + i / 2] = bf16_bits_rn(gv[i]) | (bf16_bits_rn(gv[i + 1]) << 16);
+                ku[8 * c + i / 2] = bf16_bits_rn(uv[i]) | (bf16_bits_rn(uv[i + 1]) << 16);
               }
             }
           }
-          if (c == 128 / kCols - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) dn_arrive_remote(acc_empty0 + 8 * buf);
+          dn_store_block<2, 16>(act, buf_s, p.out, row0, p.M, p.N, col0, p.N, vec);
+          if constexpr (EPI == kEpiGlu)
+            if (p.y) {
+              dn_store_block<2, 16>(kg, buf_s, p.y, row0, p.M, 2 * p.N, col0, p.N, vec);
+              dn_store_block<2, 16>(ku, buf_s, p.y + p.N, row0, p.M, 2 * p.N, col0, p.N, vec);
+            }
+        } else {
+          constexpr int kCols = 128 / ES;            // columns of one 128-byte block of a row: 32 or 64
+#pragma unroll 1
+          for (int c = 0; c < 64 / kCols; ++c) {
+            const int tc = 64 * blk + kCols * c;
+            const long long col0 = un.tn * 256LL + (un.half > 0 ? 128 : 0) + tc;
+            uint32_t w[32];
+#pragma unroll
+            for (int q = 0; q < kCols / 32; ++q) {
+              uint32_t v[32];
+              STQ1_TMEM_LD32(acc + tc + 32 * q, v);
+              const float sw = col_scale(0, col0 + 32 * q);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float f[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  f[h] = dn_sum<I8>(v[i + h], sx, I8 ? __shfl_sync(0xffffffffu, sw, i + h) : 0.f);
+                if constexpr (ES == 4) {
+                  w[i] = __float_as_uint(f[0]);
+                  w[i + 1] = __float_as_uint(f[1]);
+                } else {
+                  w[16 * q + i / 2] = bf16_bits_rn(f[0]) | (bf16_bits_rn(f[1]) << 16);
+                }
+              }
+            }
+            if (last && c == 64 / kCols - 1) release();
+            dn_store_block<ES, 32>(w, buf_s, p.out, row0, p.M, p.N, col0, p.N, vec);
           }
-          dn_store_block<ES>(w, buf_s, p.out, row0, p.M, p.N, col0, p.N, vec);
         }
       }
     }
@@ -420,7 +522,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();
-  if (warp == 9) {
+  if (warp == kPairWarpMma) {
     tc_fence_after();
     dn_tmem_dealloc<2>(tmem, 512);
   }
@@ -431,21 +533,44 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 // ---------------------------------------------------------------------------
 
 constexpr int kSplitStages = 6;
-constexpr int kSplitThreads = 192;                  // warps 0-3 epilogue, 4 producer, 5 MMA
+constexpr int kSplitThreads = 256;                  // warps 0-3 sums, 4 producer, 5 MMA; all store
 constexpr int kSplitMax = 8;                        // pieces of K: the CTAs of one cluster
 constexpr int kSplitPitch = 132;                    // words per row of a finished piece
 constexpr int kSplitOffBar = kSplitStages * kDnStageBytes;
 constexpr int kSplitSmemBytes = 1024 + kSplitOffBar + 256;
 static_assert(kDnRows * kSplitPitch * 4 <= kSplitOffBar, "a finished piece takes the place of the stages");
 
-// Each CTA of a cluster sums its piece of K (steps [k0, k1)) in TMEM and lays
-// the 128 x 128 sums into its shared memory; each then adds up its share of
-// the rows over all pieces, in the order of the pieces, and stores them: the
-// result does not depend on which CTA comes first.
-template <int EPI, bool AMN, bool BMN, int S>
+template <bool I8, bool AMN, bool BMN>
+__device__ __forceinline__ void split_mmas(uint32_t tmem, int steps, uint32_t sbase, uint32_t bar_full,
+                                           uint32_t bar_empty) {
+  constexpr uint32_t idesc = dn_idesc<I8, AMN, BMN>(128, 128);
+  for (int it = 0; it < steps; ++it) {
+    const uint32_t s = it % kSplitStages, ph = (it / kSplitStages) & 1;
+    if (!mbar_wait_bounded(bar_full + 8 * s, ph)) break;
+    tc_fence_after();
+    const uint64_t da = dn_desc<AMN>(sbase + s * kDnStageBytes);
+    const uint64_t db = dn_desc<BMN>(sbase + s * kDnStageBytes + kDnOperandBytes);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      dn_mma<I8, 1>(tmem, da + j * dn_advance<AMN>(), db + j * dn_advance<BMN>(), idesc, (it | j) != 0);
+    tc_commit(bar_empty + 8 * s);
+  }
+}
+
+struct SplitArgs {
+  DenseArgs p[2];
+  int tiles0;                        // 128 x 128 tiles of the first product
+};
+
+// Each CTA of a cluster sums its piece of K in TMEM and lays the 128 x 128
+// sums into its shared memory; each then adds up its share of the rows over
+// all pieces, in the order of the pieces, and stores them: the result does not
+// depend on which CTA comes first.  DUAL: as in the pair kernel.
+template <int EPI, bool AMN, bool BMN, bool DUAL, int S>
 __global__ void __launch_bounds__(kSplitThreads, 1)
 dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                   const DenseArgs p) {
+                   const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b1,
+                   const __grid_constant__ SplitArgs args) {
   constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const uint32_t sraw = smem_u32(smem_raw);
@@ -454,6 +579,10 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   const uint32_t bar_full = bar, bar_empty = bar + 64, bar_acc = bar + 128, s_tmem = bar + 144;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int piece = blockIdx.y;                      // the cluster of S runs along y
+  const int prob = DUAL && static_cast<int>(blockIdx.x) >= args.tiles0 ? 1 : 0;
+  const DenseArgs& p = args.p[prob];
+  const CUtensorMap* ma = DUAL && prob ? &map_a1 : &map_a;
+  const CUtensorMap* mb = DUAL && prob ? &map_b1 : &map_b;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSplitStages; ++i) {
       mbar_init(bar_full + 8 * i, 1);
@@ -463,6 +592,10 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     fence_mbar_init();
   }
   if (warp == 5) dn_tmem_alloc<1>(s_tmem, 128);
+  if (warp == 4 && lane == 0) {
+    dn_prefetch_map(ma);
+    dn_prefetch_map(mb);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -472,7 +605,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   griddep_launch_dependents();
 
   int tm, tn;
-  dn_tile_pos(p, blockIdx.x, tm, tn);
+  dn_tile_pos(p, static_cast<int>(blockIdx.x) - (prob ? args.tiles0 : 0), tm, tn);
   const int k0 = static_cast<int>(static_cast<long long>(p.n_k) * piece / S);
   const int k1 = static_cast<int>(static_cast<long long>(p.n_k) * (piece + 1) / S);
   constexpr int kOutCols = GLU ? 64 : 128;
@@ -484,60 +617,60 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         if (!mbar_wait_bounded(bar_empty + 8 * s, (use & 1) ^ 1)) break;
         mbar_arrive_expect_tx(bar_full + 8 * s, p.a_bytes + kDnOperandBytes);
         const uint32_t dst = sbase + s * kDnStageBytes, b = bar_full + 8 * s;
-        dn_load_operand<I8, AMN, 1>(dst, &map_a, k, tm * kDnRows, b);
-        if constexpr (GLU) {
-          // 64 gate rows and the 64 up rows of the same outputs (boxes of 64 rows)
-          const int step = k * (I8 ? 128 : 64);
-          dn_load<1>(dst + kDnOperandBytes, &map_b, step, tn * 64, b);
-          dn_load<1>(dst + kDnOperandBytes + kDnOperandBytes / 2, &map_b, step, static_cast<int>(p.N) + tn * 64, b);
+        if (AMN || (DUAL && prob)) {
+          dn_load_operand<I8, true, 1>(dst, ma, k, tm * kDnRows, 2, b);
         } else {
-          dn_load_operand<I8, BMN, 1>(dst + kDnOperandBytes, &map_b, k, tn * kDnRows, b);
+          dn_load<1>(dst, ma, k * (I8 ? 128 : 64), tm * kDnRows, b);      // one box of as many rows as a tile has
+        }
+        if constexpr (GLU) {
+          // 64 gate rows and the 64 up rows of the same outputs
+          dn_load_operand<I8, BMN, 1>(dst + kDnOperandBytes, mb, k, tn * 64, 1, b);
+          dn_load_operand<I8, BMN, 1>(dst + kDnOperandBytes + kDnOperandBytes / 2, mb, k,
+                                      static_cast<int>(p.N) + tn * 64, 1, b);
+        } else {
+          dn_load_operand<I8, BMN, 1>(dst + kDnOperandBytes, mb, k, tn * kDnRows, 2, b);
         }
       }
     }
   } else if (warp == 5) {
     if (lane == 0) {
-      constexpr uint32_t idesc = dn_idesc<I8, AMN, BMN>(128, 128);
-      for (int k = k0; k < k1; ++k) {
-        const uint32_t it = k - k0, s = it % kSplitStages, ph = (it / kSplitStages) & 1;
-        if (!mbar_wait_bounded(bar_full + 8 * s, ph)) break;
-        tc_fence_after();
-        const uint64_t da = dn_desc<AMN>(sbase + s * kDnStageBytes);
-        const uint64_t db = dn_desc<BMN>(sbase + s * kDnStageBytes + kDnOperandBytes);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          dn_mma<I8, 1>(tmem, da + j * dn_advance<AMN>(), db + j * dn_advance<BMN>(), idesc, (it | j) != 0);
-        tc_commit(bar_empty + 8 * s);
-      }
+      if (DUAL && prob) split_mmas<I8, true, BMN>(tmem, k1 - k0, sbase, bar_full, bar_empty);
+      else split_mmas<I8, AMN, BMN>(tmem, k1 - k0, sbase, bar_full, bar_empty);
       tc_commit(bar_acc);                            // all MMAs so far, in the error case too
     }
-  } else {
-    // the sums to shared memory (the stages are free once the last MMA is done)
+  } else if (warp < 4) {
+    // the sums to shared memory (the stages are free once the last MMA is done); an empty piece sums to zero
     mbar_wait_bounded(bar_acc, 0);
     tc_fence_after();
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
     const uint32_t row = sbase + (32 * warp + lane) * (kSplitPitch * 4);
+    if (tm * static_cast<long long>(kDnRows) + 32 * warp < p.M) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t v[32];
-      STQ1_TMEM_LD32(lanes + 32 * c, v);
-      tmem_wait_ld();
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        STQ1_TMEM_LD32(lanes + 32 * c, v);
+        tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 32; i += 4)
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + 128 * c + 4 * i), "r"(v[i]), "r"(v[i + 1]),
-                     "r"(v[i + 2]), "r"(v[i + 3])
-                     : "memory");
+        for (int i = 0; i < 32; i += 4)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + 128 * c + 4 * i), "r"(k1 > k0 ? v[i] : 0u),
+                       "r"(k1 > k0 ? v[i + 1] : 0u), "r"(k1 > k0 ? v[i + 2] : 0u), "r"(k1 > k0 ? v[i + 3] : 0u)
+                       : "memory");
+      }
     }
   }
   tc_fence_before();
   __syncwarp();
-  cluster_sync_all();                                // every piece lies in shared memory
+  if constexpr (S > 1) cluster_sync_all();           // every piece lies in shared memory
+  else __syncthreads();
   if (warp == 5) {
     tc_fence_after();
     dn_tmem_dealloc<1>(tmem, 128);
   }
 
-  // this CTA's rows: piece, piece + S, ... ; a warp takes a row, a lane four sums (or two gate/up pairs)
+  // this CTA's rows: piece, piece + S, ... ; a warp takes kRows of them at a time, so that their reads overlap, a
+  // lane four sums of each (or two gate/up pairs)
+  constexpr int kRows = S >= 8 ? 1 : (S == 1 ? 4 : 2);
+  constexpr int kWarps = kSplitThreads / 32;
   const long long m0 = static_cast<long long>(tm) * kDnRows;
   const long long n0 = static_cast<long long>(tn) * kOutCols;
   const int rows = static_cast<int>(min(static_cast<long long>(kDnRows), p.M - m0));
@@ -550,75 +683,87 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       if (col < p.N) swa[i] = p.sw[(GLU && i >= 2 ? p.N : 0) + col];
     }
   }
-  for (int r = piece + S * warp; r < rows; r += S * (kSplitThreads / 32)) {
-    const uint32_t at = sbase + r * (kSplitPitch * 4);
-    uint32_t w[S][4], v[4];
+  for (int r0 = piece + S * warp; r0 < rows; r0 += S * kWarps * kRows) {
+    uint32_t w[kRows][S][4];
+    float sxs[kRows];
 #pragma unroll
-    for (int q = 0; q < S; ++q) {
-      const uint32_t src = dn_mapa(at, q);
+    for (int j = 0; j < kRows; ++j) {
+      const int r = min(r0 + j * S * kWarps, rows - 1);      // past the end: the last row again, not stored
+      sxs[j] = I8 ? p.sx[m0 + r] : 0.f;
+      const uint32_t at = sbase + r * (kSplitPitch * 4);
+#pragma unroll
+      for (int q = 0; q < S; ++q) {
+        const uint32_t src = S > 1 ? dn_mapa(at, q) : at;
+        uint32_t(&o)[4] = w[j][q];
+        if constexpr (GLU) {
+          asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(o[0]), "=r"(o[1]) : "r"(src + 8 * lane) : "memory");
+          asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];"
+                       : "=r"(o[2]), "=r"(o[3])
+                       : "r"(src + 256 + 8 * lane)
+                       : "memory");
+        } else {
+          asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+                       : "r"(src + 16 * lane)
+                       : "memory");
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if (r0 + j * S * kWarps >= rows) break;
+      const long long m = m0 + r0 + j * S * kWarps;
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t v = w[j][0][i];
+#pragma unroll
+        for (int q = 1; q < S; ++q) {
+          if constexpr (I8) v += w[j][q][i];
+          else v = __float_as_uint(__uint_as_float(v) + __uint_as_float(w[j][q][i]));
+        }
+        f[i] = dn_sum<I8>(v, sxs[j], swa[i]);
+      }
+      const long long col = n0 + c0;
       if constexpr (GLU) {
-        asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(w[q][0]), "=r"(w[q][1]) : "r"(src + 8 * lane) : "memory");
-        asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];"
-                     : "=r"(w[q][2]), "=r"(w[q][3])
-                     : "r"(src + 256 + 8 * lane)
-                     : "memory");
+        // N is a multiple of 8 here and c0 even, so both columns exist or neither does
+        if (col < p.N) {
+          const uint32_t a = swiglu_bf16(f[0], f[2]) | (swiglu_bf16(f[1], f[3]) << 16);
+          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + m * p.N + col) = a;
+          if constexpr (EPI == kEpiGlu)
+            if (p.y) {
+              uint16_t* yr = p.y + m * 2 * p.N + col;
+              *reinterpret_cast<uint32_t*>(yr) = bf16_bits_rn(f[0]) | (bf16_bits_rn(f[1]) << 16);
+              *reinterpret_cast<uint32_t*>(yr + p.N) = bf16_bits_rn(f[2]) | (bf16_bits_rn(f[3]) << 16);
+            }
+        }
+      } else if constexpr (EPI == kEpiI8F32) {
+        float* dst = static_cast<float*>(p.out) + m * p.N + col;
+        if (p.N % 4 == 0) {
+          if (col < p.N) *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (col + i < p.N) dst[i] = f[i];
+        }
       } else {
-        asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3])
-                     : "r"(src + 16 * lane)
-                     : "memory");
-      }
-    }
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + m * p.N + col;
+        const uint32_t lo = bf16_bits_rn(f[0]) | (bf16_bits_rn(f[1]) << 16);
+        const uint32_t hi = bf16_bits_rn(f[2]) | (bf16_bits_rn(f[3]) << 16);
+        if (p.N % 4 == 0) {
+          if (col < p.N) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+        } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = w[0][i];
-#pragma unroll
-      for (int q = 1; q < S; ++q) {
-        if constexpr (I8) v[i] += w[q][i];
-        else v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[q][i]));
-      }
-    }
-    const long long m = m0 + r;
-    const float sx = I8 ? p.sx[m] : 0.f;
-    float f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = dn_sum<I8>(v[i], sx, swa[i]);
-    const long long col = n0 + c0;
-    if constexpr (GLU) {
-      // N is a multiple of 8 here and c0 even, so both columns exist or neither does
-      if (col < p.N) {
-        const uint32_t a = swiglu_bf16(f[0], f[2]) | (swiglu_bf16(f[1], f[3]) << 16);
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + m * p.N + col) = a;
-        if constexpr (EPI == kEpiGlu)
-          if (p.y) {
-            uint16_t* yr = p.y + m * 2 * p.N + col;
-            *reinterpret_cast<uint32_t*>(yr) = bf16_bits_rn(f[0]) | (bf16_bits_rn(f[1]) << 16);
-            *reinterpret_cast<uint32_t*>(yr + p.N) = bf16_bits_rn(f[2]) | (bf16_bits_rn(f[3]) << 16);
-          }
-      }
-    } else if constexpr (EPI == kEpiI8F32) {
-      float* dst = static_cast<float*>(p.out) + m * p.N + col;
-      if (p.N % 4 == 0) {
-        if (col < p.N) *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col + i < p.N) dst[i] = f[i];
-      }
-    } else {
-      uint16_t* dst = static_cast<uint16_t*>(p.out) + m * p.N + col;
-      const uint32_t lo = bf16_bits_rn(f[0]) | (bf16_bits_rn(f[1]) << 16);
-      const uint32_t hi = bf16_bits_rn(f[2]) | (bf16_bits_rn(f[3]) << 16);
-      if (p.N % 4 == 0) {
-        if (col < p.N) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col + i < p.N) dst[i] = static_cast<uint16_t>((i < 2 ? lo : hi) >> (16 * (i & 1)));
+          for (int i = 0; i < 4; ++i)
+            if (col + i < p.N) dst[i] = static_cast<uint16_t>((i < 2 ? lo : hi) >> (16 * (i & 1)));
+        }
       }
     }
   }
-  cluster_sync_all();                                // a peer may still read this CTA's piece
+  if constexpr (S > 1) {
+    __syncwarp();
+    cluster_sync_all();                              // a peer may still read this CTA's piece
+  }
 }
 
 }  // namespace stq1

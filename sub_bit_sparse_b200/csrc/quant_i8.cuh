@@ -44,48 +44,59 @@ struct Row8<true> {
   }
 };
 
-// One CTA per row: the row's largest magnitude, then its codes.  The first
-// kKeep vectors of a thread stay in registers between the two (rows of up to
-// 8192 values are read once); longer rows read the rest again.
-template <bool F32>
+// TPR threads per row (a warp or the CTA): the row's largest magnitude, then
+// its codes.  A thread's first kKeep vectors stay in registers between the two
+// (rows of up to 8 * TPR * kKeep values are read once); longer rows read the
+// rest again.  clear: one word per row to set to zero (for a later kernel's
+// maxima), or NULL.
+template <bool F32, int TPR, int kKeep>
 __global__ void __launch_bounds__(kQi8Threads)
-quant_i8_kernel(const void* __restrict__ src, long long K, int8_t* __restrict__ q, float* __restrict__ scales) {
-  constexpr int kKeep = 4;
+quant_i8_kernel(const void* __restrict__ src, long long R, long long K, int8_t* __restrict__ q,
+                float* __restrict__ scales, uint32_t* __restrict__ clear) {
+  constexpr bool kWarp = TPR == 32;
+  static_assert(kWarp || TPR == kQi8Threads, "a row is a warp's or the CTA's");
   __shared__ uint32_t s_red[kQi8Threads / 32];
-  const long long r = blockIdx.x;
+  const long long r = kWarp ? blockIdx.x * (kQi8Threads / 32LL) + (threadIdx.x >> 5) : blockIdx.x;
+  const int at = kWarp ? threadIdx.x & 31 : threadIdx.x;
   griddep_wait();
   griddep_launch_dependents();
+  if (kWarp && r >= R) return;
   const char* row = static_cast<const char*>(src) + r * K * (F32 ? 4 : 2);
   const int nv = static_cast<int>(K / 8);
   Row8<F32> keep[kKeep];
   uint32_t m = 0u;
 #pragma unroll
   for (int j = 0; j < kKeep; ++j) {
-    const int i = threadIdx.x + j * kQi8Threads;
+    const int i = at + j * TPR;
     if (i < nv) keep[j].load(row, i);
     else keep[j].zero();
   }
 #pragma unroll
   for (int j = 0; j < kKeep; ++j) m = max(m, keep[j].amax_bits());
-  for (int i = threadIdx.x + kKeep * kQi8Threads; i < nv; i += kQi8Threads) {
+  for (int i = at + kKeep * TPR; i < nv; i += TPR) {
     Row8<F32> v;
     v.load(row, i);
     m = max(m, v.amax_bits());
   }
   m = __reduce_max_sync(0xffffffffu, m);
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = m;
-  __syncthreads();
+  if constexpr (!kWarp) {
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = m;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kQi8Threads / 32; ++i) m = max(m, s_red[i]);
+    for (int i = 0; i < kQi8Threads / 32; ++i) m = max(m, s_red[i]);
+  }
   const I8Scale sc = i8_scale(m);
-  if (threadIdx.x == 0) scales[r] = sc.scale;
+  if (at == 0) {
+    scales[r] = sc.scale;
+    if (clear) clear[r] = 0u;
+  }
   uint2* out = reinterpret_cast<uint2*>(q + r * K);
 #pragma unroll
   for (int j = 0; j < kKeep; ++j) {
-    const int i = threadIdx.x + j * kQi8Threads;
+    const int i = at + j * TPR;
     if (i < nv) out[i] = keep[j].codes(sc.inv);
   }
-  for (int i = threadIdx.x + kKeep * kQi8Threads; i < nv; i += kQi8Threads) {
+  for (int i = at + kKeep * TPR; i < nv; i += TPR) {
     Row8<F32> v;
     v.load(row, i);
     out[i] = v.codes(sc.inv);
