@@ -34,6 +34,23 @@ bool make_operand_map(CUtensorMap* map, const void* base, bool i8, long long row
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D map over results [rows, cols] (row stride ld elements) for copies of
+// blocks of 32 rows by `width` bytes; a map that cannot be (a row's bytes are
+// no multiple of 16) is left as it is, and the kernel does not use it.
+bool make_result_map(CUtensorMap* map, void* base, bool f32, long long rows, long long cols, long long ld, int width) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const int es = f32 ? 4 : 2;
+  if (!base || cols * es % 16) return true;
+  cuuint64_t gdim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t gstride[1] = {static_cast<cuuint64_t>(ld) * es};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(width / es), 32};
+  cuuint32_t es1[2] = {1, 1};
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, gdim, gstride, box,
+            es1, CU_TENSOR_MAP_INTERLEAVE_NONE, width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 std::atomic<bool> g_dense_configured[kMaxDevices];
 constexpr int kFewAllSmem = 232448;
 template <int EPI, int CODES, int MT, int NT>
@@ -159,6 +176,13 @@ int launch_pairs(const DenseProduct& d0, const DenseProduct& d1, cudaStream_t s)
     if (tiles[i] >= (1LL << 29)) return STQ1_ERR_SHAPE;
     args.p[i] = tile_args<I8>(*d[i], tm, tn, kDnRows);
   }
+  CUtensorMap o0{}, o1{}, o2{};
+  constexpr int kWidth = GLU ? 64 : 128;
+  if (!make_result_map(&o0, d0.out, EPI == kEpiI8F32, d0.M, d0.N, d0.N, kWidth)) return STQ1_ERR_CUDA;
+  if (DUAL && !make_result_map(&o1, d1.out, false, d1.M, d1.N, d1.N, kWidth)) return STQ1_ERR_CUDA;
+  if (EPI == kEpiGlu && d0.y && !(make_result_map(&o1, d0.y, false, d0.M, d0.N, 2 * d0.N, kWidth) &&
+                                  make_result_map(&o2, d0.y + d0.N, false, d0.M, d0.N, 2 * d0.N, kWidth)))
+    return STQ1_ERR_CUDA;
   const int clusters = sm_count() / 2;
   args.tiles0 = static_cast<int>(tiles[0]);
   args.tiles = static_cast<int>(tiles[0] + tiles[1]);
@@ -167,7 +191,7 @@ int launch_pairs(const DenseProduct& d0, const DenseProduct& d1, cudaStream_t s)
   args.full = 2 * rest <= clusters ? args.tiles - rest : args.tiles;
   const int units = args.full + 2 * (args.tiles - args.full);
   return launch_pdl(dense_pair_kernel<EPI, AMN, BMN, DUAL>, 2u * static_cast<unsigned>(std::min(units, clusters)),
-                    kPairThreads, kPairSmemBytes, s, a0, b0, a1, b1, args);
+                    kPairThreads, kPairSmemBytes, s, a0, b0, a1, b1, o0, o1, o2, args);
 }
 
 // Pieces of K for so many tiles of n_k steps: as many as run at once, two steps each at least.

@@ -190,61 +190,79 @@ __device__ __forceinline__ void dn_tile_pos(const DenseArgs& p, int tile, int& t
 // Large products: pairs of CTAs on 256 x 256 tiles.
 // ---------------------------------------------------------------------------
 
-// (Five stages measure the same as six, four are 5-9% slower; sixteen epilogue
-// warps with five stages the same for bf16 results and 5% slower for fp32.)
+// (Four stages are 5-9% slower; five with two result blocks per epilogue warp 1-4%.)
 constexpr int kPairStages = 6;
 constexpr int kPairEpi = 8;                         // epilogue warps: TMEM quadrants x column blocks in turn
 constexpr int kPairSides = kPairEpi / 4;
 constexpr int kPairWarpA = kPairEpi, kPairWarpMma = kPairEpi + 1, kPairWarpB = kPairEpi + 2;
 constexpr int kPairThreads = 32 * (kPairEpi + 3);
 constexpr int kPairOffStage = kPairStages * kDnStageBytes;
-constexpr int kPairOffBar = kPairOffStage + kPairEpi * 4096;
+constexpr int kPairOffBar = kPairOffStage + kPairEpi * 4096;     // a block of results per epilogue warp
 constexpr int kPairSmemBytes = 1024 + kPairOffBar + 256;
 static_assert(kPairSmemBytes <= 232448, "shared memory per CTA is at most 227 KB");
 
-// One warp's 32 rows of WORDS words (row = lane) to global memory through
-// shared memory: 16-byte pieces at piece ^ (row & 7) (of four pieces, & 3),
-// so that neither the row-wise stores nor the reads of whole rows meet on a
-// bank; then WORDS / 4 lanes store a row's piece each.  ES: bytes of an
-// element; a word holds 4 / ES.
-template <int ES, int WORDS>
-__device__ __forceinline__ void dn_store_block(const uint32_t* w, uint32_t buf, void* out, long long row0,
-                                               long long rows, long long ld, long long col0, long long cols, bool vec) {
+// One warp's block of results: 32 rows (row = lane) of WORDS words, in shared
+// memory as the tensor copies' swizzle wants it (rows of 128 bytes: 16-byte
+// piece c at c ^ (row & 7); of 64: at c ^ ((row >> 1) & 3)), so that the
+// row-wise stores do not meet on a bank, then by one tensor copy to global
+// memory, which drops what lies past the edges.  The copy runs while the warp
+// computes its next block.  (With reads of whole rows and 16-byte stores in its
+// place the fp32 results of [4096, 512] x [512, 7168] took 50 us instead of 34.)
+template <int WORDS>
+__device__ __forceinline__ uint32_t dn_place(int row, int piece) {
+  return row * (WORDS * 4) + ((piece ^ (WORDS == 32 ? row & 7 : (row >> 1) & 3)) << 4);
+}
+template <int WORDS>
+__device__ __forceinline__ void dn_block_to_smem(const uint32_t* w, uint32_t buf) {
   const int lane = threadIdx.x & 31;
-  constexpr int kPer = 4 / ES;                      // elements per word
-  constexpr int kPieces = WORDS / 4, kPitch = WORDS * 4, kRows = 32 / kPieces;
-  // with four pieces two rows share 128 bytes: rows r and r + 1 keep apart by
-  // themselves, rows r and r + 2 by the swizzle
-  auto place = [](int row, int piece) {
-    return row * kPitch + ((piece ^ (kPieces == 8 ? row & 7 : (row >> 1) & 3)) << 4);
-  };
-  __syncwarp();                                     // the previous block's reads are done
 #pragma unroll
-  for (int c = 0; c < kPieces; ++c)
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(buf + place(lane, c)), "r"(w[4 * c]), "r"(w[4 * c + 1]),
-                 "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+  for (int c = 0; c < WORDS / 4; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(buf + dn_place<WORDS>(lane, c)), "r"(w[4 * c]),
+                 "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
                  : "memory");
+}
+template <int WORDS>
+__device__ __forceinline__ void dn_store_copy(const uint32_t* w, uint32_t buf, const CUtensorMap* map, int x, int y) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+  dn_block_to_smem<WORDS>(w, buf);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(buf)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+// The same for rows that tensor copies cannot address (a row's bytes are no
+// multiple of 16): element by element.
+template <int ES, int WORDS>
+__device__ __forceinline__ void dn_store_plain(const uint32_t* w, uint32_t buf, void* out, long long row0,
+                                               long long rows, long long ld, long long col0, long long cols) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPer = 4 / ES, kPieces = WORDS / 4;
+  __syncwarp();                                     // the previous block's reads are done
+  dn_block_to_smem<WORDS>(w, buf);
   __syncwarp();
   char* base = static_cast<char*>(out);
   const int piece = lane % kPieces;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    const int r = kRows * i + lane / kPieces;
+    const int r = (32 / kPieces) * i + lane / kPieces;
     if (row0 + r >= rows) continue;
-    const uint4 v = lds_v4(buf + place(r, piece));
+    const uint4 v = lds_v4(buf + dn_place<WORDS>(r, piece));
     const long long c = col0 + piece * 4 * kPer;
     char* dst = base + ((row0 + r) * ld + c) * ES;
-    if (vec) {
-      if (c < cols) *reinterpret_cast<uint4*>(dst) = v;       // cols is then a multiple of 16 / ES
-    } else {
-      const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int j = 0; j < 4 * kPer; ++j)
-        if (c + j < cols) {
-          if constexpr (ES == 4) reinterpret_cast<uint32_t*>(dst)[j] = e[j];
-          else reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>(e[j >> 1] >> (16 * (j & 1)));
-        }
-    }
+    for (int j = 0; j < 4 * kPer; ++j)
+      if (c + j < cols) {
+        if constexpr (ES == 4) reinterpret_cast<uint32_t*>(dst)[j] = e[j];
+        else reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>(e[j >> 1] >> (16 * (j & 1)));
+      }
   }
 }
 
@@ -311,12 +329,15 @@ __device__ __forceinline__ bool pair_loads(const CUtensorMap* map, int n_k, int 
   return true;
 }
 
-// DUAL: the second product's A is MN-major (dW beside dX).
+// DUAL: the second product's A is MN-major (dW beside dX).  map_o: the result;
+// map_o1, map_o2: the second product's result (DUAL), or the gate and up halves
+// of y (kEpiGlu).
 template <int EPI, bool AMN, bool BMN, bool DUAL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b1,
-                  const __grid_constant__ PairArgs args) {
+                  const __grid_constant__ CUtensorMap map_o, const __grid_constant__ CUtensorMap map_o1,
+                  const __grid_constant__ CUtensorMap map_o2, const __grid_constant__ PairArgs args) {
   constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
   static_assert(!(I8 && (AMN || BMN)), "8-bit operands are K-major");
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -416,105 +437,116 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     // ---- epilogue: warp w reads TMEM lanes 32 (w & 3).. and every kPairSides-th block of columns ----
     const int quad = warp & 3, side = warp >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-    const uint32_t buf_s = sbase + kPairOffStage + warp * 4096;
+    const uint32_t buf0 = sbase + kPairOffStage + warp * 4096;
     const uint32_t acc_empty0 = dn_mapa(bar_acc_empty, 0);
     constexpr int ES = EPI == kEpiI8F32 ? 4 : 2;
+    constexpr int kMine = 4 / kPairSides;            // column blocks of a whole tile that are this warp's
     uint32_t t = 0;
     for (int unit = first; unit < n_units; unit += stride, ++t) {
       const uint32_t buf = t & 1, use = t >> 1;
       const PairUnit un = pair_unit<DUAL>(args, unit);
       const DenseArgs& p = args.p[un.prob];
-      const bool vec = p.N % (16 / ES) == 0;
+      const bool copies = p.N % (16 / ES) == 0;
+      const CUtensorMap* mo = DUAL && un.prob ? &map_o1 : &map_o;
       const long long row0 = un.tm * 256LL + rank * kDnRows + 32 * quad;
+      const bool rows_in = row0 < p.M;
       const float sx = I8 && row0 + lane < p.M ? p.sx[row0 + lane] : 0.f;
+      // blocks of 64 columns of B: four of a whole tile, two of a half
+      const int blocks = un.half < 0 ? 4 : 2;
+      // the first output of a block, and the scales of its weight rows (fetched before the wait for the sums)
+      auto first_col = [&](int blk) -> long long {
+        if constexpr (GLU) return un.tn * 128LL + 32 * blk + (un.half > 0 ? 64 : 0);
+        else return un.tn * 256LL + 64 * blk + (un.half > 0 ? 128 : 0);
+      };
+      float scale[kMine][2] = {};
+      if constexpr (I8) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const long long c = first_col(side + i * kPairSides) + lane;
+          if (GLU) {
+            if (c < p.N) scale[i][0] = p.sw[c], scale[i][1] = p.sw[p.N + c];
+          } else {
+            if (c < p.N) scale[i][0] = p.sw[c];
+            if (c + 32 < p.N) scale[i][1] = p.sw[c + 32];
+          }
+        }
+      }
       if (!mbar_wait_bounded(bar_acc_full + 8 * buf, use & 1)) break;
       tc_fence_after();
       const uint32_t acc = lanes + 256 * buf;
-      // scale of column col0 + lane of B (0 past the end)
-      auto col_scale = [&](long long first_row, long long col0) {
-        return I8 && col0 + lane < p.N ? p.sw[first_row + col0 + lane] : 0.f;
-      };
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) dn_arrive_remote(acc_empty0 + 8 * buf);
       };
-      // blocks of 64 columns of B: four of a whole tile, two of a half
-      const int blocks = un.half < 0 ? 4 : 2;
-#pragma unroll 1
-      for (int blk = side; blk < blocks; blk += kPairSides) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int blk = side + i * kPairSides;
+        if (blk >= blocks) break;
         const bool last = blk + kPairSides >= blocks;
+        const long long col0 = first_col(blk);
+        const bool in = rows_in && col0 < p.N;
+        const int x = static_cast<int>(col0), y = static_cast<int>(row0);
+        uint32_t v0[32], v1[32];
+        // gated: 32 gate sums and, `up` further, the 32 up sums of the same outputs; else 64 sums
+        STQ1_TMEM_LD32(acc + (GLU ? 32 : 64) * blk, v0);
+        STQ1_TMEM_LD32(acc + (GLU ? (un.half < 0 ? 128 : 64) + 32 * blk : 64 * blk + 32), v1);
+        tmem_wait_ld();
+        if (last) release();
+        auto sum0 = [&](int j) { return dn_sum<I8>(v0[j], sx, I8 ? __shfl_sync(0xffffffffu, scale[i][0], j) : 0.f); };
+        auto sum1 = [&](int j) { return dn_sum<I8>(v1[j], sx, I8 ? __shfl_sync(0xffffffffu, scale[i][1], j) : 0.f); };
         if constexpr (GLU) {
-          // 32 outputs: gate sums in columns from c0, up sums `up` further
-          const int c0 = 32 * blk, up = un.half < 0 ? 128 : 64;
-          const long long col0 = un.tn * 128LL + c0 + (un.half > 0 ? 64 : 0);
-          float swg = 0.f, swu = 0.f;
-          if constexpr (I8) {
-            swg = col_scale(0, col0);
-            swu = col_scale(p.N, col0);
-          }
-          uint32_t gs[32], us[32];
-          STQ1_TMEM_LD32(acc + c0, gs);
-          STQ1_TMEM_LD32(acc + up + c0, us);
-          tmem_wait_ld();
-          if (last) release();
           uint32_t act[16], kg[16], ku[16];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float gv[16], uv[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              gv[i] = dn_sum<I8>(gs[16 * c + i], sx, I8 ? __shfl_sync(0xffffffffu, swg, 16 * c + i) : 0.f);
-              uv[i] = dn_sum<I8>(us[16 * c + i], sx, I8 ? __shfl_sync(0xffffffffu, swu, 16 * c + i) : 0.f);
+            for (int j = 0; j < 16; ++j) {
+              gv[j] = sum0(16 * c + j);
+              uv[j] = sum1(16 * c + j);
             }
             swiglu_bf16_pack<16>(gv, uv, act + 8 * c);
             if constexpr (EPI == kEpiGlu) {
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                kg[8 * c + i / 2] = bf16_bits_rn(gv[i]) | (bf16_bits_rn(gv[i + 1]) << 16);
-                ku[8 * c + i / 2] = bf16_bits_rn(uv[i]) | (bf16_bits_rn(uv[i + 1]) << 16);
+              for (int j = 0; j < 16; j += 2) {
+                kg[8 * c + j / 2] = bf16_bits_rn(gv[j]) | (bf16_bits_rn(gv[j + 1]) << 16);
+                ku[8 * c + j / 2] = bf16_bits_rn(uv[j]) | (bf16_bits_rn(uv[j + 1]) << 16);
               }
             }
           }
-          dn_store_block<2, 16>(act, buf_s, p.out, row0, p.M, p.N, col0, p.N, vec);
-          if constexpr (EPI == kEpiGlu)
-            if (p.y) {
-              dn_store_block<2, 16>(kg, buf_s, p.y, row0, p.M, 2 * p.N, col0, p.N, vec);
-              dn_store_block<2, 16>(ku, buf_s, p.y + p.N, row0, p.M, 2 * p.N, col0, p.N, vec);
+          // N is a multiple of 8: rows are always whole pieces of 16 bytes
+          if (in) {
+            dn_store_copy<16>(act, buf0, mo, x, y);
+            if (EPI == kEpiGlu && p.y) {
+              dn_store_copy<16>(kg, buf0, &map_o1, x, y);
+              dn_store_copy<16>(ku, buf0, &map_o2, x, y);
             }
-        } else {
-          constexpr int kCols = 128 / ES;            // columns of one 128-byte block of a row: 32 or 64
-#pragma unroll 1
-          for (int c = 0; c < 64 / kCols; ++c) {
-            const int tc = 64 * blk + kCols * c;
-            const long long col0 = un.tn * 256LL + (un.half > 0 ? 128 : 0) + tc;
+          }
+        } else if constexpr (ES == 4) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
             uint32_t w[32];
 #pragma unroll
-            for (int q = 0; q < kCols / 32; ++q) {
-              uint32_t v[32];
-              STQ1_TMEM_LD32(acc + tc + 32 * q, v);
-              const float sw = col_scale(0, col0 + 32 * q);
-              tmem_wait_ld();
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(h ? sum1(j) : sum0(j));
+            if (!rows_in || col0 + 32 * h >= p.N) continue;
+            if (copies) dn_store_copy<32>(w, buf0, mo, x + 32 * h, y);
+            else dn_store_plain<4, 32>(w, buf0, p.out, row0, p.M, p.N, col0 + 32 * h, p.N);
+          }
+        } else {
+          uint32_t w[32];
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float f[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  f[h] = dn_sum<I8>(v[i + h], sx, I8 ? __shfl_sync(0xffffffffu, sw, i + h) : 0.f);
-                if constexpr (ES == 4) {
-                  w[i] = __float_as_uint(f[0]);
-                  w[i + 1] = __float_as_uint(f[1]);
-                } else {
-                  w[16 * q + i / 2] = bf16_bits_rn(f[0]) | (bf16_bits_rn(f[1]) << 16);
-                }
-              }
-            }
-            if (last && c == 64 / kCols - 1) release();
-            dn_store_block<ES, 32>(w, buf_s, p.out, row0, p.M, p.N, col0, p.N, vec);
+          for (int j = 0; j < 32; j += 2) {
+            w[j / 2] = bf16_bits_rn(sum0(j)) | (bf16_bits_rn(sum0(j + 1)) << 16);
+            w[16 + j / 2] = bf16_bits_rn(sum1(j)) | (bf16_bits_rn(sum1(j + 1)) << 16);
+          }
+          if (in) {
+            if (copies) dn_store_copy<32>(w, buf0, mo, x, y);
+            else dn_store_plain<2, 32>(w, buf0, p.out, row0, p.M, p.N, col0, p.N);
           }
         }
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   // all roles of both CTAs meet here (every wait above is bounded): the
