@@ -556,77 +556,37 @@ def ep_combine(rows, inv, t: int, topk: int, out=None):
 # ---------------------------------------------------------------------------
 
 
-# Outputs are made with empty_like and empty_strided, which are quicker than new_empty (1.1 against 1.7 us a call).
+# The marshalling of these calls is compiled (binding/dense_calls.cpp): they are
+# short, and from Python it took twice as long as the launch itself.  The
+# extension checks every operand (type, shape, contiguous, one device), makes
+# the outputs that are not given, and calls the C ABI on the current stream with
+# the operands' device current.
+
+_dense_mod = None
 
 
-def _matrix(t, dtype, name):
-    """The shape of a contiguous CUDA matrix of that dtype."""
-    _require(t, dtype, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
-    return t.shape
-
-
-def _operand(t, dtype, shape, dev, name):
-    """Checks a contiguous CUDA tensor of that dtype and shape on device index ``dev``; returns its address."""
-    if getattr(t, "dtype", None) is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _require(t, dtype, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} is on cuda:{t.get_device()}, the other operands on cuda:{dev}")
-
-
-_get_device = None
-
-
-def _current_device() -> int:
-    global _get_device
-    if _get_device is None:
-        # torch's raw getter, as for the stream
-        torch = _torch()
-        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-    return _get_device()
-
-
-def _call(name: str, dev: int, *args):
-    """Calls a library function with device ``dev`` current; raises on an error code."""
-    fn = getattr(_lib if _lib is not None else _load(), name)
-    if _current_device() == dev:
-        rc = fn(*args)
-    else:
-        with _torch().cuda.device(dev):
-            rc = fn(*args)
-    if rc:
-        _check(name, rc)
-
-
-def _scratch(ws, nbytes, ref, dev):
-    # a tensor of its own for each call, so that calls on two streams, or captured in two graphs, never share one
-    torch = _torch()
-    if ws is None:
-        return torch.empty_strided((max(nbytes, 16),), (1,), dtype=torch.uint8, device=ref.device)
-    _require(ws, torch.uint8, "ws")
-    if ws.get_device() != dev:
-        raise ValueError("ws must be on the operands' device")
-    return ws
+def _dense():
+    """The compiled marshalling, bound to the loaded library; raises ImportError if it is missing."""
+    global _dense_mod
+    if _dense_mod is None:
+        lib = _load()
+        _torch()                                             # its libraries first
+        path = os.path.join(_HERE, "_dense_calls.so")
+        if not os.path.exists(path):
+            raise ImportError(f"_dense_calls.so not found at {path}; build it with "
+                              "`python -m sub_bit_sparse_b200.build`")
+        from . import _dense_calls
+        names = ("stq1_quantize_i8", "stq1_i8_matmul", "stq1_i8_ffn_workspace", "stq1_i8_ffn", "stq1_glu",
+                 "stq1_glu_backward_workspace", "stq1_glu_backward")
+        _dense_calls.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names), Stq1Error)
+        _dense_mod = _dense_calls
+    return _dense_mod
 
 
 def quantize_i8(src, out=None, scales=None):
     """bf16 or fp32 rows [R, K] -> (int8 codes [R, K], fp32 scales [R]): per-token codes of activations
     or per-channel codes of weights."""
-    torch = _torch()
-    f32 = getattr(src, "dtype", None) is torch.float32
-    r, k = _matrix(src, torch.float32 if f32 else torch.bfloat16, "src")
-    dev = src.get_device()
-    if out is None:
-        out = torch.empty_like(src, dtype=torch.int8)
-    if scales is None:
-        scales = torch.empty_strided((r,), (1,), dtype=torch.float32, device=src.device)
-    _call("stq1_quantize_i8", dev, src.data_ptr(), TYPE_F32 if f32 else TYPE_BF16, r, k,
-          _operand(out, torch.int8, (r, k), dev, "out"), _operand(scales, torch.float32, (r,), dev, "scales"),
-          _stream(src))
-    return out, scales
+    return (_dense_mod or _dense()).quantize_i8(src, out, scales)
 
 
 def i8_matmul(x_q, x_scales, w_q, w_scales, out=None, dtype=None):
@@ -634,82 +594,32 @@ def i8_matmul(x_q, x_scales, w_q, w_scales, out=None, dtype=None):
 
     dtype: torch.float32 (default) or torch.bfloat16; taken from ``out`` when that is given."""
     torch = _torch()
-    t, k = _matrix(x_q, torch.int8, "x_q")
-    n = w_q.shape[0] if getattr(w_q, "ndim", 0) == 2 else _matrix(w_q, torch.int8, "w_q")[0]
-    dev = x_q.get_device()
     if dtype is None:
         dtype = torch.float32 if out is None else out.dtype
-    if dtype not in (torch.float32, torch.bfloat16):
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise TypeError(f"i8_matmul gives torch.float32 or torch.bfloat16, not {dtype}")
-    if out is None:
-        out = torch.empty_strided((t, n), (n, 1), dtype=dtype, device=x_q.device)
-    _call("stq1_i8_matmul", dev, x_q.data_ptr(),
-          _operand(x_scales, torch.float32, (t,), dev, "x_scales"), _operand(w_q, torch.int8, (n, k), dev, "w_q"),
-          _operand(w_scales, torch.float32, (n,), dev, "w_scales"), _operand(out, dtype, (t, n), dev, "out"),
-          TYPE_F32 if dtype is torch.float32 else TYPE_BF16, t, n, k, _stream(x_q))
-    return out
+    return (_dense_mod or _dense()).i8_matmul(x_q, x_scales, w_q, w_scales, out, dtype is torch.bfloat16)
 
 
 def i8_ffn(x, gateup_q, gateup_scales, down_q, down_scales, out=None, ws=None):
-    """Gated feed-forward layer at 8 bits: bf16 x [T, H], int8 gate/up [N, H] and down [H, N/2] -> fp32 [T, H]."""
-    torch = _torch()
-    t, h = _matrix(x, torch.bfloat16, "x")
-    n = gateup_q.shape[0] if getattr(gateup_q, "ndim", 0) == 2 else _matrix(gateup_q, torch.int8, "gateup_q")[0]
-    dev = x.get_device()
-    if out is None:
-        out = torch.empty_like(x, dtype=torch.float32)
-    args = (x.data_ptr(), _operand(gateup_q, torch.int8, (n, h), dev, "gateup_q"),
-            _operand(gateup_scales, torch.float32, (n,), dev, "gateup_scales"),
-            _operand(down_q, torch.int8, (h, n // 2), dev, "down_q"),
-            _operand(down_scales, torch.float32, (h,), dev, "down_scales"),
-            _operand(out, torch.float32, (t, h), dev, "out"))
-    ws = _scratch(ws, _load().stq1_i8_ffn_workspace(t, n, h) if ws is None else 0, x, dev)
-    _call("stq1_i8_ffn", dev, *args, t, n, h, ws.data_ptr(), ws.numel(), _stream(x))
-    return out
+    """Gated feed-forward layer at 8 bits: bf16 x [T, H], int8 gate/up [N, H] and down [H, N/2] -> fp32 [T, H].
+
+    ws: uint8 workspace of stq1_i8_ffn_workspace bytes; by default one of the call's own."""
+    return (_dense_mod or _dense()).i8_ffn(x, gateup_q, gateup_scales, down_q, down_scales, out, ws)
 
 
 def glu(x, w, save: bool = False, out=None, y=None):
     """act [T, N/2] = SiLU(x Wg^T) * (x Wu^T), bf16, for bf16 x [T, K] and the fused w [N, K] (gate rows, then
-    up rows).  With ``save`` returns (act, y): y [T, N] bf16 is what glu_backward needs."""
-    torch = _torch()
-    t, k = _matrix(x, torch.bfloat16, "x")
-    n = w.shape[0] if getattr(w, "ndim", 0) == 2 else _matrix(w, torch.bfloat16, "w")[0]
-    dev = x.get_device()
-    save = save or y is not None
-    if out is None:
-        out = torch.empty_strided((t, n // 2), (n // 2, 1), dtype=torch.bfloat16, device=x.device)
-    if save and y is None:
-        y = torch.empty_strided((t, n), (n, 1), dtype=torch.bfloat16, device=x.device)
-    _call("stq1_glu", dev, x.data_ptr(), _operand(w, torch.bfloat16, (n, k), dev, "w"),
-          _operand(out, torch.bfloat16, (t, n // 2), dev, "out"),
-          _operand(y, torch.bfloat16, (t, n), dev, "y") if save else None, t, n, k, _stream(x))
-    return (out, y) if save else out
+    up rows).  With ``save`` (or a ``y`` to fill) returns (act, y): y [T, N] bf16 is what glu_backward needs."""
+    return (_dense_mod or _dense()).glu(x, w, bool(save) or y is not None, out, y)
 
 
 def glu_backward(dact, y, x, w, dx=None, dw=None, need_dx: bool = True, need_dw: bool = True, ws=None):
     """Gradients of glu: (dx [T, K], dw [N, K]) in bf16 from dact [T, N/2], the kept y [T, N], x [T, K] and
-    w [N, K]; None in the place of one that is not needed.  x may be None without dw, w without dx."""
-    torch = _torch()
-    t, n = _matrix(y, torch.bfloat16, "y")
-    if not (need_dx or need_dw):
-        raise ValueError("glu_backward: nothing to compute")
-    if need_dx and w is None or need_dw and x is None:
-        raise ValueError("dx needs w, and dw needs x")
-    k = _matrix(x, torch.bfloat16, "x")[1] if x is not None else _matrix(w, torch.bfloat16, "w")[1]
-    dev = y.get_device()
-    dx = None if not need_dx else dx if dx is not None else y.new_empty((t, k)) if x is None else torch.empty_like(x)
-    dw = None if not need_dw else dw if dw is not None else y.new_empty((n, k)) if w is None else torch.empty_like(w)
-    at = lambda v, shape, name: None if v is None else _operand(v, torch.bfloat16, shape, dev, name)  # noqa: E731
-    args = (_operand(dact, torch.bfloat16, (t, n // 2), dev, "dact"), y.data_ptr(), at(x, (t, k), "x"),
-            at(w, (n, k), "w"), at(dx, (t, k), "dx"), at(dw, (n, k), "dw"))
-    if ws is None:                                  # the workspace is dY: [T, N] bf16, as y
-        ws = torch.empty_like(y)
-        nbytes = t * n * 2
-    else:
-        ws = _scratch(ws, 0, y, dev)
-        nbytes = ws.numel()
-    _call("stq1_glu_backward", dev, *args, t, n, k, ws.data_ptr(), nbytes, _stream(y))
-    return dx, dw
+    w [N, K]; None in the place of one that is not needed.  x may be None without dw, w without dx.
+
+    ws: uint8 workspace of stq1_glu_backward_workspace bytes; by default one of the call's own."""
+    return (_dense_mod or _dense()).glu_backward(dact, y, x, w, dx, dw, bool(need_dx), bool(need_dw), ws)
 
 
 PATH_AUTO, PATH_TABLE, PATH_TILES, PATH_MMA = 0, 1, 2, 3

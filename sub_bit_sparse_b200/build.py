@@ -8,6 +8,9 @@ library does not depend on the runtime version torch ships.
 compiled with STQ1_DEBUG: its kernels bounds-check the indices they read
 and record STQ1_DEV_BOUNDS instead of accessing out of range.  Importing the
 package with STQ1_DEBUG=1 in the environment loads that library.
+
+``build_binding()`` (part of ``build()``) compiles binding/dense_calls.cpp, the
+argument marshalling of the 8-bit and gated calls, against the installed torch.
 """
 
 from __future__ import annotations
@@ -22,6 +25,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libstq1.so")
 LIB_DEBUG = os.path.join(HERE, "libstq1_debug.so")
+BINDING_SRC = os.path.join(HERE, "binding", "dense_calls.cpp")
+BINDING = os.path.join(HERE, "_dense_calls.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -62,10 +67,32 @@ def up_to_date(debug: bool = False) -> bool:
     return all(os.path.getmtime(f) <= t for f in cu + cpp + hdr + [__file__])
 
 
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    """Compile the CPython extension _dense_calls.so (g++, torch's headers); returns its path."""
+    inputs = [BINDING_SRC, os.path.join(INCLUDE, "stq1.h"), __file__]
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-pthread",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[a for p in include_paths() for a in ("-isystem", p)], "-isystem", sysconfig.get_paths()["include"],
+          "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
+          *["-L" + p for p in library_paths()], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ltorch"], verbose)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = False, debug: bool = False) -> str:
     """Compile every source under csrc/ into libstq1.so (libstq1_debug.so with
-    debug=True); returns its path."""
+    debug=True), and the binding extension; returns the library's path."""
     lib = LIB_DEBUG if debug else LIB
+    build_binding(verbose, force and not debug)
     if not force and up_to_date(debug):
         return lib
     nvcc = _nvcc()
