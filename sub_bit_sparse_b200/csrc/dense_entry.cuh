@@ -11,7 +11,6 @@ namespace stq1 {
 namespace {
 
 constexpr long long kDenseMaxDim = 1LL << 30;
-constexpr int kFfnFusedTokens = 4;
 constexpr long long kI8MaxK = 131056;    // 128 * 128 * K stays below 2^31
 
 bool dense_shape_ok(long long a, long long b, long long c) {
@@ -53,15 +52,15 @@ bool make_result_map(CUtensorMap* map, void* base, bool f32, long long rows, lon
 
 std::atomic<bool> g_dense_configured[kMaxDevices];
 constexpr int kFewAllSmem = 232448;
-template <int EPI, int CODES, int MT, int NT>
+template <int EPI, bool MADE, int MT, int NT>
 bool few_config_one() {
-  return cudaFuncSetAttribute(dense_few_kernel<EPI, CODES, MT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(dense_few_kernel<EPI, MADE, MT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kFewAllSmem) == cudaSuccess;
 }
-template <int EPI, int CODES>
+template <int EPI, bool MADE>
 bool few_config() {
-  return few_config_one<EPI, CODES, 2, 1>() && few_config_one<EPI, CODES, 2, 2>() && few_config_one<EPI, CODES, 4, 1>() &&
-         few_config_one<EPI, CODES, 4, 2>();
+  return few_config_one<EPI, MADE, 2, 1>() && few_config_one<EPI, MADE, 2, 2>() && few_config_one<EPI, MADE, 4, 1>() &&
+         few_config_one<EPI, MADE, 4, 2>();
 }
 std::atomic<int> g_max_clusters[kMaxDevices][4];   // clusters of 1, 2, 4, 8 CTAs of the split kernel that run at once
 template <int EPI, bool AMN, bool BMN, bool DUAL, int S>
@@ -108,9 +107,8 @@ int ensure_dense_configured() {
         tile_config<kEpiI8Glu, false, false, false>() && tile_config<kEpiGlu, false, false, false>() &&
         tile_config<kEpiBf16, false, true, false>() && tile_config<kEpiBf16, true, true, false>() &&
         tile_config<kEpiBf16, false, true, true>() &&
-        few_config<kEpiI8F32, kCodesGiven>() && few_config<kEpiI8F32, kCodesMade>() &&
-        few_config<kEpiI8F32, kCodesMadeKnown>() && few_config<kEpiI8Bf16, kCodesGiven>() &&
-        few_config<kEpiI8Glu, kCodesGiven>() && few_config<kEpiI8Glu, kCodesMade>() && few_config<kEpiGlu, kCodesGiven>())) {
+        few_config<kEpiI8F32, false>() && few_config<kEpiI8F32, true>() && few_config<kEpiI8Bf16, false>() &&
+        few_config<kEpiI8Glu, false>() && few_config<kEpiGlu, false>())) {
     cudaGetLastError();
     return STQ1_ERR_CUDA;
   }
@@ -266,17 +264,9 @@ bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu) 
   return true;
 }
 
-// What ran or runs around a streaming product: `early`, the kernel before does
-// not write its weights; `next`, the weights that the kernel after reads.
-struct FewChain {
-  bool early;
-  const void* next;
-  long long next_bytes;
-  uint32_t* amax;                    // see FewArgs
-};
-
-template <int EPI, int CODES>
-int launch_few(const FewPlan& f, const DenseProduct& d, const FewChain& c, cudaStream_t s) {
+// early: the kernel before does not write the weights.  amax: see FewArgs.
+template <int EPI, bool MADE>
+int launch_few(const FewPlan& f, const DenseProduct& d, bool early, uint32_t* amax, cudaStream_t s) {
   constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
   int rc = ensure_dense_configured();
   if (rc != STQ1_OK) return rc;
@@ -293,17 +283,15 @@ int launch_few(const FewPlan& f, const DenseProduct& d, const FewChain& c, cudaS
   p.pad = f.pad;
   p.n_k = f.n_k;
   p.n_slots = f.n_slots;
-  p.early = c.early;
-  p.amax = c.amax;
-  p.next = static_cast<const char*>(c.next);
-  p.next_bytes = c.next_bytes;
+  p.early = early;
+  p.amax = amax;
   CUtensorMap mw;
   if (!make_operand_map(&mw, d.b, I8, GLU ? 2 * d.N : d.N, d.K, f.rows)) return STQ1_ERR_CUDA;
   const unsigned grid = static_cast<unsigned>((d.N + f.rows - 1) / f.rows);
   auto launch = [&](auto kernel) { return launch_pdl(kernel, grid, kFewThreads, f.smem, s, mw, p); };
   if (f.pad > 32)
-    return d.M > 8 ? launch(dense_few_kernel<EPI, CODES, 4, 2>) : launch(dense_few_kernel<EPI, CODES, 4, 1>);
-  return d.M > 8 ? launch(dense_few_kernel<EPI, CODES, 2, 2>) : launch(dense_few_kernel<EPI, CODES, 2, 1>);
+    return d.M > 8 ? launch(dense_few_kernel<EPI, MADE, 4, 2>) : launch(dense_few_kernel<EPI, MADE, 4, 1>);
+  return d.M > 8 ? launch(dense_few_kernel<EPI, MADE, 2, 2>) : launch(dense_few_kernel<EPI, MADE, 2, 1>);
 }
 
 // A product of K-major operands: few tokens take the streaming kernel.
@@ -311,7 +299,7 @@ template <int EPI>
 int launch_product(const DenseProduct& d, cudaStream_t s) {
   FewPlan f;
   if (plan_few(&f, d.M, d.N, d.K * (epi_i8(EPI) ? 1 : 2), epi_glu(EPI)))
-    return launch_few<EPI, kCodesGiven>(f, d, FewChain{}, s);
+    return launch_few<EPI, false>(f, d, false, nullptr, s);
   return launch_tiles<EPI, false, false>(d, s);
 }
 
@@ -463,23 +451,15 @@ extern "C" int stq1_i8_ffn(const uint16_t* x, const int8_t* gateup_q, const floa
   const DenseProduct down = i8_product(aq, sa, down_q, down_scales, out, T, H, N / 2);
   FewPlan fg, fd;
   if (plan_few(&fg, T, N / 2, H, true) && plan_few(&fd, T, H, N / 2, false)) {
-    // few tokens: each kernel streams its weights while the one before it
-    // still runs, and the first brings the second's into L2
-    const long long next_bytes = static_cast<long long>(H) * (N / 2);
+    // few tokens: each kernel asks for its weights while the one before it
+    // still runs; the activation's maxima are kept by the kernel that writes
+    // it, so that its codes are made inside the second product
+    uint32_t* amax = reinterpret_cast<uint32_t*>(sa);
     DenseProduct dn = down;
     dn.a = act;
-    int rc;
-    if (T <= kFfnFusedTokens) {           // codes made inside both products: two launches
-      DenseProduct u = up;
-      u.a = x;
-      rc = launch_few<kEpiI8Glu, kCodesMade>(fg, u, FewChain{false, down_q, next_bytes, nullptr}, s);
-      return rc != STQ1_OK ? rc : launch_few<kEpiI8F32, kCodesMade>(fd, dn, FewChain{true, nullptr, 0, nullptr}, s);
-    }
-    // the activation's maxima are kept by the kernel that writes it
-    uint32_t* amax = reinterpret_cast<uint32_t*>(sa);
-    rc = launch_quant_i8(x, STQ1_TYPE_BF16, T, H, xq, sx, s, amax);
-    if (rc == STQ1_OK) rc = launch_few<kEpiI8Glu, kCodesGiven>(fg, up, FewChain{true, down_q, next_bytes, amax}, s);
-    return rc != STQ1_OK ? rc : launch_few<kEpiI8F32, kCodesMadeKnown>(fd, dn, FewChain{true, nullptr, 0, amax}, s);
+    int rc = launch_quant_i8(x, STQ1_TYPE_BF16, T, H, xq, sx, s, amax);
+    if (rc == STQ1_OK) rc = launch_few<kEpiI8Glu, false>(fg, up, true, amax, s);
+    return rc != STQ1_OK ? rc : launch_few<kEpiI8F32, true>(fd, dn, true, amax, s);
   }
   int rc = launch_quant_i8(x, STQ1_TYPE_BF16, T, H, xq, sx, s);
   if (rc != STQ1_OK) return rc;

@@ -46,10 +46,8 @@ struct FewArgs {
   int n_k;                     // 128-byte steps of K
   int n_slots;
   int early;                   // the weights are not written by the kernel before: load them at once
-  uint32_t* amax;              // fp32 bits of each token's largest magnitude: of x, read (kCodesMadeKnown);
-                               // of the gated output, raised (8-bit gated form), or NULL
-  const char* next;            // weights of the kernel after, brought into L2 at the end, or NULL
-  long long next_bytes;
+  uint32_t* amax;              // fp32 bits of each token's largest magnitude: of x, read (MADE); of the
+                               // output, raised (8-bit gated form), or NULL
 };
 
 // Bytes between tokens in shared memory: whole steps and 16 more, so that two
@@ -69,18 +67,17 @@ __device__ __forceinline__ void few_mma(float (&c)[4], uint32_t a0, uint32_t a1,
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Where the tokens' codes come from: they are given; or x is bf16 and they are
-// made here, from each token's largest magnitude, which each CTA finds for
-// itself (T * K values from L2, while its first weights are on their way) or
-// reads (the kernel that wrote x kept it).
-enum FewCodes { kCodesGiven, kCodesMade, kCodesMadeKnown };
-
+// MADE: x is bf16 and its codes are made here, from each token's largest
+// magnitude, which the kernel that wrote x kept (the down projection of the
+// 8-bit layer).  For the first projection the magnitudes would have to be found
+// by every CTA, which took longer than a launch of its own: 15.7 us against
+// 15.5 for the layer at one token, 18.9 against 16.4 at four.
 // MT: fragments of 16 weight rows (at most); NT: groups of 8 tokens.
-template <int EPI, int CODES, int MT, int NT>
+template <int EPI, bool MADE, int MT, int NT>
 __global__ void __launch_bounds__(kFewThreads, 2)
 dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
-  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI), QX = CODES != kCodesGiven;
-  static_assert(I8 || !QX, "codes are made for 8-bit weights");
+  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
+  static_assert(I8 || !MADE, "codes are made for 8-bit weights");
   using Acc = std::conditional_t<I8, int, float>;
   constexpr int ES = I8 ? 1 : 2;
   constexpr int kStep = kDnStepBytes / ES;
@@ -88,7 +85,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
   const uint32_t sraw = smem_u32(smem_raw);
   const uint32_t sbase = (sraw + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t s_max = sbase + 8 * kFewMaxSlots * kFewWarps, s_scale = s_max + 32, bar_x = s_scale + 64;
+  const uint32_t s_scale = sbase + 8 * kFewMaxSlots * kFewWarps, bar_x = s_scale + 64;
   const uint32_t slot_bytes = p.pad * kDnStepBytes;
   const uint32_t s_w = sbase + kFewHead;                               // the warps' slots
   const uint32_t s_x = s_w + kFewWarps * p.n_slots * slot_bytes;       // the tokens
@@ -121,64 +118,26 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
     for (int i = 0; i < p.n_slots && warp + kFewWarps * i < p.n_k; ++i) fetch(warp + kFewWarps * i, i);
   if (p.early) griddep_wait();
   griddep_launch_dependents();
-  // Once a warp has asked for its last step, it asks for its share of the next
-  // kernel's weights in L2, so that HBM does not rest between the two.
-  auto prefetch_next = [&]() {                                         // lane 0 only
-    const long long share = (p.next_bytes / (static_cast<long long>(gridDim.x) * kFewWarps) + 16) & ~15LL;
-    long long at = share * (blockIdx.x * static_cast<long long>(kFewWarps) + warp);
-    const long long end = min(at + share, p.next_bytes);
-    for (; at < end; at += 4096)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.next + at),
-                   "r"(static_cast<uint32_t>(min(4096LL, end - at)))
-                   : "memory");
-  };
-  if (lane == 0 && p.next && warp + kFewWarps * p.n_slots >= p.n_k) prefetch_next();
-
   // ---- the tokens into shared memory ----
   const long long kbytes = p.K * ES;
-  if constexpr (QX) {
-    // 8 / n warps per token, n = T rounded up to a power of two (two rounds for more than 8 tokens)
-    const int n = p.T <= 1 ? 1 : (p.T <= 2 ? 2 : (p.T <= 4 ? 4 : 8));
-    const int per = kFewWarps / n, first = (warp % per) * 32 + lane;
+  if constexpr (MADE) {
+    // the warps share out the tokens: one warp each, or with fewer tokens 2, 4 or 8
+    const int per = p.T > 4 ? 1 : (p.T > 2 ? 2 : (p.T > 1 ? 4 : 8));
     const int nv = static_cast<int>(p.K / 16);
-    for (int tok0 = 0; tok0 < p.T; tok0 += 8) {
-      const int tok = tok0 + warp / per;
+    for (int tok = warp / per; tok < p.T; tok += kFewWarps / per) {
       const char* xr = static_cast<const char*>(p.x) + tok * p.K * 2;
-      uint32_t m = 0u;
-      if (CODES == kCodesMadeKnown) {
-        m = tok < p.T ? __ldcg(p.amax + tok) : 0u;
-      } else if (tok < p.T) {
+      const I8Scale sc = i8_scale(__ldcg(p.amax + tok));
+      const int first = (warp % per) * 32 + lane;
+      if (first == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_scale + 4 * tok), "f"(sc.scale) : "memory");
 #pragma unroll 4
-        for (int i = first; i < nv; i += 32 * per) {
-          Row8<false> a, b;
-          a.load(xr, 2 * i);
-          b.load(xr, 2 * i + 1);
-          m = max(m, max(a.amax_bits(), b.amax_bits()));
-        }
-      }
-      if (CODES == kCodesMade) m = __reduce_max_sync(0xffffffffu, m);
-      if (CODES == kCodesMade && per > 1) {
-        if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(s_max + 4 * warp), "r"(m) : "memory");
-        __syncthreads();
-        for (int i = 0; i < per; ++i) {
-          uint32_t o;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(o) : "r"(s_max + 4 * (warp / per * per + i)));
-          m = max(m, o);
-        }
-      }
-      const I8Scale sc = i8_scale(m);
-      if (tok < p.T) {
-        if (first == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_scale + 4 * tok), "f"(sc.scale) : "memory");
-#pragma unroll 4
-        for (int i = first; i < nv; i += 32 * per) {
-          Row8<false> a, b;
-          a.load(xr, 2 * i);
-          b.load(xr, 2 * i + 1);
-          const uint2 lo = a.codes(sc.inv), hi = b.codes(sc.inv);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(s_x + tok * pitch + 16 * i), "r"(lo.x), "r"(lo.y),
-                       "r"(hi.x), "r"(hi.y)
-                       : "memory");
-        }
+      for (int i = first; i < nv; i += 32 * per) {
+        Row8<false> a, b;
+        a.load(xr, 2 * i);
+        b.load(xr, 2 * i + 1);
+        const uint2 lo = a.codes(sc.inv), hi = b.codes(sc.inv);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(s_x + tok * pitch + 16 * i), "r"(lo.x), "r"(lo.y),
+                     "r"(hi.x), "r"(hi.y)
+                     : "memory");
       }
     }
   } else {
@@ -197,7 +156,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
                    : "memory");
   }
   __syncthreads();
-  bool ok = QX || mbar_wait_bounded(bar_x, 0);
+  bool ok = MADE || mbar_wait_bounded(bar_x, 0);
 
   // ---- this warp's steps ----
   const int mt = p.pad >> 4;
@@ -240,10 +199,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
     }
     __syncwarp();                                    // every lane has read the slot
     const int next = step + kFewWarps * p.n_slots;
-    if (lane == 0 && next < p.n_k) {
-      fetch(next, slot);
-      if (p.next && next + kFewWarps >= p.n_k) prefetch_next();
-    }
+    if (lane == 0 && next < p.n_k) fetch(next, slot);
     if (++slot == p.n_slots) slot = 0, ph ^= 1;
   }
   __syncthreads();                                   // the slots are free: the warps' sums take their place
@@ -281,7 +237,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
     };
     const long long n = n0 + r;
     float sx = 0.f;
-    if constexpr (QX) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sx) : "r"(s_scale + 4 * tok));
+    if constexpr (MADE) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sx) : "r"(s_scale + 4 * tok));
     else if constexpr (I8) sx = p.sx[tok];
     auto value = [&](Acc v, long long row) -> float {
       if constexpr (I8) return i8_value(v, sx, p.sw[row]);
