@@ -586,9 +586,12 @@ int stq1_mix_allocate(const double* err_low, const double* err_high, const doubl
  * Common to them: row-major contiguous buffers, caller-owned, 16-byte aligned
  * unless noted (scales: 4 bytes).  Every size is at most 2^30 and every
  * product of two of a call's sizes at most 2^40, else STQ1_ERR_SHAPE.
- * Results do not depend on the other rows of a call, and two calls with the
- * same inputs and sizes give the same bits.  Nothing but the outputs and the
- * workspace is written.
+ * Two calls with the same inputs and sizes give the same bits (sums that are
+ * split are joined in a fixed order), and a row's results do not depend on what
+ * the other rows hold.  Nothing but the outputs and the workspace is written.
+ * No index is taken from device memory, so the debug build checks nothing more
+ * here.  The kernel is chosen by the sizes: up to 16 tokens a streaming kernel
+ * (mma.sync), else tensor-core tiles (tcgen05).
  */
 
 /* Element types of stq1_quantize_i8's source and stq1_i8_matmul's result. */
@@ -636,8 +639,8 @@ int stq1_i8_matmul(const int8_t* xq, const float* x_scales, const int8_t* wq, co
  *   (xq, sx) = stq1_quantize_i8(x);  y = stq1_i8_matmul(xq, gate/up) in fp32;
  *   act = stq1_swiglu(y);  (aq, sa) = stq1_quantize_i8(act);
  *   out = stq1_i8_matmul(aq, down) in fp32,
- * with the bits of that chain of calls; y and, for few tokens, the codes are
- * never stored.
+ * with the bits of that chain of calls; y and, for up to 16 tokens, the
+ * activation's codes are never stored.
  *   x              device, [T, H] bf16 bits.
  *   gateup_q, gateup_scales  device, [N, H] codes (gate rows 0..N/2-1, up rows
  *                  N/2..N-1) and [N] fp32.

@@ -1,5 +1,9 @@
 """8-bit integer codes, products and the 8-bit gated layer against the oracle, bit for bit (needs a B200)."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -86,6 +90,7 @@ SHAPES = [  # T, N, K: every token count where a kernel changes, and its neighbo
     (33, 128, 144), (48, 1030, 1024), (64, 255, 640), (65, 257, 640), (77, 2053, 2048), (100, 3, 64), (127, 128, 128),
     (128, 4096, 2048), (129, 130, 112), (200, 1000, 3600), (255, 512, 16), (256, 256, 512), (257, 259, 272),
     (300, 4096, 1024), (512, 777, 1296), (700, 2048, 512), (1000, 1025, 1040), (1500, 4096, 256), (2049, 513, 384),
+    (2500, 1001, 272), (2500, 1004, 64), (2561, 2056, 16), (5000, 600, 144), (4100, 4098, 48), (20000, 130, 32),
 ]
 
 
@@ -222,6 +227,50 @@ def test_captured_layer_follows_its_inputs(t):
     graphs[1].replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], eager[2]) and torch.equal(outs[1], eager[1])
+
+
+def test_first_call_of_a_process_may_be_captured():
+    code = """
+import sys; sys.path.insert(0, %r)
+import torch, sub_bit_sparse_b200 as stq1
+x = torch.randint(-127, 128, (5, 512), dtype=torch.int8, device="cuda")
+w = torch.randint(-127, 128, (40, 512), dtype=torch.int8, device="cuda")
+sx, sw, y = torch.ones(5, device="cuda"), torch.ones(40, device="cuda"), torch.zeros(5, 40, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    stq1.i8_matmul(x, sx, w, sw, out=y)
+g.replay()
+assert torch.equal(y.double(), x.double() @ w.double().T) and stq1.status() == 0
+print("OK")
+""" % os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert res.stdout.strip().endswith("OK"), res.stdout + res.stderr
+
+
+def test_weights_coded_just_before_the_layer():
+    """Codes of new weights and the layer that reads them, back to back on one stream, again and again."""
+    rng = np.random.default_rng(11)
+    n, h = 1024, 1536
+    for t in (1, 7, 16, 40):
+        x = _bf16(rng.standard_normal((t, h)))[0]
+        fw = [torch.randn(n, h, device="cuda") / h ** 0.5 for _ in range(4)]
+        fd = [torch.randn(h, n // 2, device="cuda") / (n // 2) ** 0.5 for _ in range(4)]
+        want = []
+        for a, b in zip(fw, fd):
+            gu, dn = stq1.quantize_i8(a), stq1.quantize_i8(b)
+            torch.cuda.synchronize()
+            want.append(stq1.i8_ffn(x, *gu, *dn))
+        gu, dn = stq1.quantize_i8(fw[0]), stq1.quantize_i8(fd[0])
+        torch.cuda.synchronize()
+        for _ in range(3):
+            got = []
+            for a, b in zip(fw, fd):
+                stq1.quantize_i8(b, out=dn[0], scales=dn[1])
+                stq1.quantize_i8(a, out=gu[0], scales=gu[1])
+                got.append(stq1.i8_ffn(x, *gu, *dn))
+            torch.cuda.synchronize()
+            assert all(torch.equal(g, w) for g, w in zip(got, want)), t
 
 
 def test_two_streams_at_once():
