@@ -184,7 +184,8 @@ int launch_pairs(const DenseProduct& d0, const DenseProduct& d1, cudaStream_t s)
   const int clusters = sm_count() / 2;
   args.tiles0 = static_cast<int>(tiles[0]);
   args.tiles = static_cast<int>(tiles[0] + tiles[1]);
-  // a last round that would leave more than half of the pairs idle goes by half tiles
+  // a last round that would leave more than half of the pairs idle goes by half
+  // tiles: 1% at 4096 tokens by [4096, 7168] (81.9 us against 82.9)
   const int rest = args.tiles % clusters;
   args.full = 2 * rest <= clusters ? args.tiles - rest : args.tiles;
   const int units = args.full + 2 * (args.tiles - args.full);
@@ -192,7 +193,9 @@ int launch_pairs(const DenseProduct& d0, const DenseProduct& d1, cudaStream_t s)
                     kPairThreads, kPairSmemBytes, s, a0, b0, a1, b1, o0, o1, o2, args);
 }
 
-// Pieces of K for so many tiles of n_k steps: as many as run at once, two steps each at least.
+// Pieces of K for so many tiles of n_k steps: as many as run at once, two steps
+// each at least.  (Clusters of eight for 17 tiles, of which the GPCs hold 16 at a
+// time: 9.3 us for [2053, 2048] weights and 77 tokens; clusters of four: 5.6.)
 int split_pieces(long long tiles, int n_k) {
   const int dev = current_device();
   int S = 1;
@@ -230,7 +233,10 @@ int launch_split(const DenseProduct& d0, const DenseProduct& d1, int S, cudaStre
   }
 }
 
-// More 128 x 128 tiles than SMs: pairs on 256 x 256 tiles; else one tile per CTA, K split.
+// More 128 x 128 tiles than SMs: pairs on 256 x 256 tiles; else one tile per
+// CTA, K split.  At the border, int8 with [4096, 7168] weights: 512 tokens (128
+// tiles) take 19.1 us split and 20.2 on pairs, 600 tokens (160 tiles, two rounds
+// of single tiles) 24.4 us on pairs.
 template <int EPI, bool AMN, bool BMN>
 int launch_tiles(const DenseProduct& d, cudaStream_t s) {
   int rc = ensure_dense_configured();
@@ -294,7 +300,8 @@ int launch_few(const FewPlan& f, const DenseProduct& d, bool early, uint32_t* am
   return d.M > 8 ? launch(dense_few_kernel<EPI, MADE, 2, 2>) : launch(dense_few_kernel<EPI, MADE, 2, 1>);
 }
 
-// A product of K-major operands: few tokens take the streaming kernel.
+// A product of K-major operands: few tokens take the streaming kernel (int8,
+// [4096, 7168]: 6.2 us at one token, 7.1 at 16; the split kernel 7.4 and 7.7).
 template <int EPI>
 int launch_product(const DenseProduct& d, cudaStream_t s) {
   FewPlan f;
@@ -303,16 +310,23 @@ int launch_product(const DenseProduct& d, cudaStream_t s) {
   return launch_tiles<EPI, false, false>(d, s);
 }
 
-// Rows of up to 2048 values take a warp each (from 1024 on with eight vectors in flight per lane), longer ones a CTA.
+// Threads per row by its length, so that enough rows are in flight; measured on
+// 4096 bf16 rows, against the next larger choice: 256 values 2.2 us (2.9), 1024
+// 2.8 (3.4), 2048 5.5 (9.7), 4096 8.8 (10.6), 7168 14.4 (15.6); with fp32 rows
+// the last step turns round, 7168 values 22.4 us with 256 threads (23.3 with 128).
 template <bool F32>
 int launch_quant_rows(const void* src, long long R, long long K, int8_t* q, float* scales, uint32_t* clear,
                       cudaStream_t s) {
-  constexpr int kPer = kQi8Threads / 32;
-  const unsigned warps = static_cast<unsigned>((R + kPer - 1) / kPer);
-  if (K <= 1024) return launch_pdl(quant_i8_kernel<F32, 32, 4>, warps, kQi8Threads, 0, s, src, R, K, q, scales, clear);
-  if (K <= 2048) return launch_pdl(quant_i8_kernel<F32, 32, 8>, warps, kQi8Threads, 0, s, src, R, K, q, scales, clear);
-  return launch_pdl(quant_i8_kernel<F32, kQi8Threads, 4>, static_cast<unsigned>(R), kQi8Threads, 0, s, src, R, K, q,
-                    scales, clear);
+  const unsigned warps = static_cast<unsigned>((R + kQi8Warps - 1) / kQi8Warps), rows = static_cast<unsigned>(R);
+  auto launch = [&](auto kernel, unsigned grid, int threads) {
+    return launch_pdl(kernel, grid, static_cast<unsigned>(threads), 0, s, src, R, K, q, scales, clear);
+  };
+  if (K <= 1024) return launch(quant_i8_kernel<F32, 32, 4>, warps, 32 * kQi8Warps);
+  if (K <= 2048) return launch(quant_i8_kernel<F32, 32, 8>, warps, 32 * kQi8Warps);
+  if (K <= 4096) return launch(quant_i8_kernel<F32, 128, 4>, rows, 128);
+  if constexpr (!F32)
+    if (K <= 8192) return launch(quant_i8_kernel<F32, 128, 8>, rows, 128);
+  return launch(quant_i8_kernel<F32, 256, 4>, rows, 256);
 }
 int launch_quant_i8(const void* src, int type, long long R, long long K, int8_t* q, float* scales, cudaStream_t s,
                     uint32_t* clear = nullptr) {

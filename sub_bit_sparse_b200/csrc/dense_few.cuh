@@ -7,7 +7,13 @@
 // copies into slots of its own and contracts them with mma.sync.  (tcgen05
 // is no help here: an MMA reads 64 or 128 rows of A whatever the tokens, and
 // with 32 weight rows a step's four MMAs take longer than its bytes from HBM:
-// 13 us against 7 on [4096, 7168].)
+// 13 us against 6 on [4096, 7168] int8.)
+//
+// Bound by HBM and by what a launch cannot avoid, about 3 us from its start to
+// the first bytes and from the last bytes to the stored sums: bf16 gated
+// [4096, 7168] at one token 12.0 us, 4.9 TB/s (58.7 MB alone would take 8.9);
+// int8 6.2 us at one token, 7.1 at 16.  (Loads straight into registers instead of
+// copies through shared memory: 7.7 and 14.3 us at one token.)
 //
 // A contraction may take its k in any order as long as both operands agree on
 // it.  So a lane's share of an A fragment need not be the 4-byte pieces that

@@ -187,7 +187,21 @@ __device__ __forceinline__ void dn_tile_pos(const DenseArgs& p, int tile, int& t
 }
 
 // ---------------------------------------------------------------------------
-// Large products: pairs of CTAs on 256 x 256 tiles.
+// Large products: pairs of CTAs on 256 x 256 tiles, one pair per two SMs, each
+// working through its tiles.  Per 128-byte step of K a CTA copies 128 rows of A
+// and 128 of B (32 KB) and the pair's four MMAs (M = N = 256) take 512 cycles,
+// so that L2 has to deliver 64 bytes a clock and SM; a smaller tile would need
+// more.  The sums of one tile are stored while the next one's are formed (two
+// accumulators of 256 columns are all of TMEM).
+//   warps 0-7   epilogue
+//   warps 8, 10 producers of A and of B (one thread for both is too slow where
+//               an operand takes four copies a step: 340 us became 372 for the
+//               two gradients of 4096 tokens by [4096, 7168])
+//   warp 9      MMAs of the pair (leader)
+// Bound by the tensor pipe and, in a sustained loop, by the power limit: int8
+// 4096 tokens by [4096, 7168] 80-82 us cold (2.95 PFLOP/s), 95 sustained at
+// lower clocks, 70 with all codes zero; tensor pipe 76% of the active cycles,
+// the rest start, last epilogue and an uneven last round.
 // ---------------------------------------------------------------------------
 
 // (Four stages are 5-9% slower; five with two result blocks per epilogue warp 1-4%.)
@@ -561,7 +575,11 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// Products with few tiles: one CTA per 128 x 128 tile and piece of K.
+// Products with few tiles: one CTA per 128 x 128 tile and piece of K.  Bound by
+// the copies into shared memory: 32 KB per step in 436 cycles (75 bytes a clock)
+// where the MMAs take 256; below about 128 tokens by the weights' way from HBM.
+// [4096, 7168] int8: 8.9 us at 64 tokens, 10.2 at 128, 13.1 at 256, 19.1 at 512.
+// (Prefetching the weights into L2 as well, from idle warps, is 5-18% slower.)
 // ---------------------------------------------------------------------------
 
 constexpr int kSplitStages = 6;

@@ -5,7 +5,7 @@
 
 namespace stq1 {
 
-constexpr int kQi8Threads = 256;
+constexpr int kQi8Warps = 8;       // rows per CTA where a row is a warp's
 
 // Eight consecutive values of a row as fp32 and the largest magnitude's bits.
 template <bool F32>
@@ -44,19 +44,21 @@ struct Row8<true> {
   }
 };
 
-// TPR threads per row (a warp or the CTA): the row's largest magnitude, then
-// its codes.  A thread's first kKeep vectors stay in registers between the two
-// (rows of up to 8 * TPR * kKeep values are read once); longer rows read the
-// rest again.  clear: one word per row to set to zero (for a later kernel's
-// maxima), or NULL.
+// TPR threads per row (a warp, or a CTA of that size): the row's largest
+// magnitude, then its codes.  A thread's first kKeep vectors stay in registers
+// between the two (rows of up to 8 * TPR * kKeep values are read once); longer
+// rows read the rest again.  clear: one word per row to set to zero (for a
+// later kernel's maxima), or NULL.
+//
+// Bound by HBM when the rows are many ([4096, 7168] fp32: 22.5 us, 6.5 TB/s,
+// the copy rate), by latency when they are few ([16, 7168]: 1.7 us).
 template <bool F32, int TPR, int kKeep>
-__global__ void __launch_bounds__(kQi8Threads)
+__global__ void __launch_bounds__(TPR == 32 ? 32 * kQi8Warps : TPR)
 quant_i8_kernel(const void* __restrict__ src, long long R, long long K, int8_t* __restrict__ q,
                 float* __restrict__ scales, uint32_t* __restrict__ clear) {
   constexpr bool kWarp = TPR == 32;
-  static_assert(kWarp || TPR == kQi8Threads, "a row is a warp's or the CTA's");
-  __shared__ uint32_t s_red[kQi8Threads / 32];
-  const long long r = kWarp ? blockIdx.x * (kQi8Threads / 32LL) + (threadIdx.x >> 5) : blockIdx.x;
+  __shared__ uint32_t s_red[kWarp ? 1 : TPR / 32];
+  const long long r = kWarp ? blockIdx.x * static_cast<long long>(kQi8Warps) + (threadIdx.x >> 5) : blockIdx.x;
   const int at = kWarp ? threadIdx.x & 31 : threadIdx.x;
   griddep_wait();
   griddep_launch_dependents();
@@ -83,7 +85,7 @@ quant_i8_kernel(const void* __restrict__ src, long long R, long long K, int8_t* 
     if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kQi8Threads / 32; ++i) m = max(m, s_red[i]);
+    for (int i = 0; i < TPR / 32; ++i) m = max(m, s_red[i]);
   }
   const I8Scale sc = i8_scale(m);
   if (at == 0) {
