@@ -181,16 +181,30 @@ int launch_pairs(const DenseProduct& d0, const DenseProduct& d1, cudaStream_t s)
   if (EPI == kEpiGlu && d0.y && !(make_result_map(&o1, d0.y, false, d0.M, d0.N, 2 * d0.N, kWidth) &&
                                   make_result_map(&o2, d0.y + d0.N, false, d0.M, d0.N, 2 * d0.N, kWidth)))
     return STQ1_ERR_CUDA;
-  const int clusters = sm_count() / 2;
-  args.tiles0 = static_cast<int>(tiles[0]);
-  args.tiles = static_cast<int>(tiles[0] + tiles[1]);
+  const int pairs = sm_count() / 2;
+  int rest_tiles = static_cast<int>(tiles[0]);       // of the list's last part
+  if (DUAL) {
+    args.long_prob = args.p[0].n_k >= args.p[1].n_k ? 0 : 1;
+    const int other = 1 - args.long_prob;
+    args.long_tiles = static_cast<int>(tiles[args.long_prob]);
+    args.late = args.long_tiles % pairs;
+    rest_tiles = static_cast<int>(tiles[other]);
+    const int short_of = pairs - args.late;          // pairs with one long tile fewer (all, if the tiles came out even)
+    // (a tile weighs at least its epilogue, about 12 steps: 300 tokens by [4096,
+    // 7168], whose short tiles have 5, take 49 us so and 60 by the steps alone)
+    auto weight = [&](int i) { return std::max(args.p[i].n_k, 12); };
+    args.lead = args.late ? std::min(weight(args.long_prob) / weight(other), rest_tiles / short_of) : 0;
+    rest_tiles -= args.lead * short_of;
+  }
   // a last round that would leave more than half of the pairs idle goes by half
   // tiles: 1% at 4096 tokens by [4096, 7168] (81.9 us against 82.9)
-  const int rest = args.tiles % clusters;
-  args.full = 2 * rest <= clusters ? args.tiles - rest : args.tiles;
-  const int units = args.full + 2 * (args.tiles - args.full);
-  return launch_pdl(dense_pair_kernel<EPI, AMN, BMN, DUAL>, 2u * static_cast<unsigned>(std::min(units, clusters)),
-                    kPairThreads, kPairSmemBytes, s, a0, b0, a1, b1, o0, o1, o2, args);
+  const int last = rest_tiles % pairs, done = (DUAL ? args.lead * (pairs - args.late) : 0) + rest_tiles - last;
+  args.full = 2 * last <= pairs ? done : done + last;
+  args.units = args.full + (2 * last <= pairs ? 2 * last : 0);
+  // one product: no more pairs than units.  Two always run on all pairs: the list is laid out for them.
+  const int grid = DUAL ? pairs : std::min(args.units, pairs);
+  return launch_pdl(dense_pair_kernel<EPI, AMN, BMN, DUAL>, 2u * static_cast<unsigned>(grid), kPairThreads,
+                    kPairSmemBytes, s, a0, b0, a1, b1, o0, o1, o2, args);
 }
 
 // Pieces of K for so many tiles of n_k steps: as many as run at once, two steps
