@@ -219,7 +219,7 @@ int split_pieces(long long tiles, int n_k) {
 }
 
 template <int EPI, bool AMN, bool BMN, bool DUAL>
-int launch_split(const DenseProduct& d0, const DenseProduct& d1, int S, cudaStream_t s) {
+int launch_split(const DenseProduct& d0, const DenseProduct& d1, int S, bool early, cudaStream_t s) {
   constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
   // a lone row of tiles copies no more rows of A than there are (the sums of the others are never stored)
   const int a_rows = !AMN && d0.M < kDnRows ? static_cast<int>((d0.M + 7) / 8 * 8) : kDnRows;
@@ -229,6 +229,7 @@ int launch_split(const DenseProduct& d0, const DenseProduct& d1, int S, cudaStre
   const DenseProduct* d[2] = {&d0, &d1};
   long long tiles = 0;
   SplitArgs args{};
+  args.early = early;
   for (int i = 0; i < (DUAL ? 2 : 1); ++i) {
     const long long tm = (d[i]->M + 127) / 128, tn = ((GLU ? 2 * d[i]->N : d[i]->N) + 127) / 128;
     if (i == 1) args.tiles0 = static_cast<int>(tiles);
@@ -252,11 +253,11 @@ int launch_split(const DenseProduct& d0, const DenseProduct& d1, int S, cudaStre
 // tiles) take 19.1 us split and 20.2 on pairs, 600 tokens (160 tiles, two rounds
 // of single tiles) 24.4 us on pairs.
 template <int EPI, bool AMN, bool BMN>
-int launch_tiles(const DenseProduct& d, cudaStream_t s) {
+int launch_tiles(const DenseProduct& d, bool early, cudaStream_t s) {
   int rc = ensure_dense_configured();
   if (rc != STQ1_OK) return rc;
   if (single_tiles<epi_glu(EPI)>(d) > sm_count()) return launch_pairs<EPI, AMN, BMN, false>(d, d, s);
-  return launch_split<EPI, AMN, BMN, false>(d, d, split_pieces(single_tiles<epi_glu(EPI)>(d), k_steps(d.K, epi_i8(EPI))), s);
+  return launch_split<EPI, AMN, BMN, false>(d, d, split_pieces(single_tiles<epi_glu(EPI)>(d), k_steps(d.K, epi_i8(EPI))), early, s);
 }
 
 // How a product with few tokens is laid out: outputs per CTA so that every SM
@@ -317,11 +318,11 @@ int launch_few(const FewPlan& f, const DenseProduct& d, bool early, uint32_t* am
 // A product of K-major operands: few tokens take the streaming kernel (int8,
 // [4096, 7168]: 6.2 us at one token, 7.1 at 16; the split kernel 7.4 and 7.7).
 template <int EPI>
-int launch_product(const DenseProduct& d, cudaStream_t s) {
+int launch_product(const DenseProduct& d, bool early, cudaStream_t s) {
   FewPlan f;
   if (plan_few(&f, d.M, d.N, d.K * (epi_i8(EPI) ? 1 : 2), epi_glu(EPI)))
-    return launch_few<EPI, false>(f, d, false, nullptr, s);
-  return launch_tiles<EPI, false, false>(d, s);
+    return launch_few<EPI, false>(f, d, early, nullptr, s);
+  return launch_tiles<EPI, false, false>(d, early, s);
 }
 
 // Threads per row by its length, so that enough rows are in flight; measured on
@@ -399,7 +400,7 @@ extern "C" int stq1_i8_matmul(const int8_t* xq, const float* x_scales, const int
     return STQ1_ERR_ALIGN;
   const DenseProduct p = i8_product(xq, x_scales, wq, w_scales, y, T, N, K);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return type == STQ1_TYPE_F32 ? launch_product<kEpiI8F32>(p, s) : launch_product<kEpiI8Bf16>(p, s);
+  return type == STQ1_TYPE_F32 ? launch_product<kEpiI8F32>(p, false, s) : launch_product<kEpiI8Bf16>(p, false, s);
 }
 
 extern "C" int stq1_glu(const uint16_t* x, const uint16_t* W, uint16_t* act, uint16_t* y, int64_t T, int64_t N,
@@ -408,7 +409,7 @@ extern "C" int stq1_glu(const uint16_t* x, const uint16_t* W, uint16_t* act, uin
   if (!x || !W || !act) return STQ1_ERR_NULL;
   if (!glu_shape_ok(T, N, K)) return STQ1_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(W) || !aligned16(act) || !aligned16(y)) return STQ1_ERR_ALIGN;
-  return launch_product<kEpiGlu>({x, W, T, N / 2, K, nullptr, nullptr, act, y}, static_cast<cudaStream_t>(stream));
+  return launch_product<kEpiGlu>({x, W, T, N / 2, K, nullptr, nullptr, act, y}, false, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t stq1_glu_backward_workspace(int64_t T, int64_t N, int64_t K) {
@@ -441,16 +442,16 @@ extern "C" int stq1_glu_backward(const uint16_t* dact, const uint16_t* y, const 
   const long long tx = single_tiles<false>(px), tw = single_tiles<false>(pw);
   if (tx + tw <= sm_count()) {
     const int S = split_pieces(tx + tw, std::max(k_steps(N, false), k_steps(T, false)));
-    if (dx && dW) return launch_split<kEpiBf16, false, true, true>(px, pw, S, s);
-    return dx ? launch_split<kEpiBf16, false, true, false>(px, px, S, s)
-              : launch_split<kEpiBf16, true, true, false>(pw, pw, S, s);
+    if (dx && dW) return launch_split<kEpiBf16, false, true, true>(px, pw, S, false, s);
+    return dx ? launch_split<kEpiBf16, false, true, false>(px, px, S, false, s)
+              : launch_split<kEpiBf16, true, true, false>(pw, pw, S, false, s);
   }
   if (dx && dW && tx > sm_count() && tw > sm_count()) return launch_pairs<kEpiBf16, false, true, true>(px, pw, s);
   if (dx) {
-    rc = launch_tiles<kEpiBf16, false, true>(px, s);
+    rc = launch_tiles<kEpiBf16, false, true>(px, false, s);
     if (rc != STQ1_OK) return rc;
   }
-  return dW ? launch_tiles<kEpiBf16, true, true>(pw, s) : rc;
+  return dW ? launch_tiles<kEpiBf16, true, true>(pw, false, s) : rc;
 }
 
 extern "C" size_t stq1_i8_ffn_workspace(int64_t T, int64_t N, int64_t H) {
@@ -491,9 +492,9 @@ extern "C" int stq1_i8_ffn(const uint16_t* x, const int8_t* gateup_q, const floa
   }
   int rc = launch_quant_i8(x, STQ1_TYPE_BF16, T, H, xq, sx, s);
   if (rc != STQ1_OK) return rc;
-  rc = launch_product<kEpiI8Glu>(up, s);
+  rc = launch_product<kEpiI8Glu>(up, true, s);
   if (rc != STQ1_OK) return rc;
   rc = launch_quant_i8(act, STQ1_TYPE_BF16, T, N / 2, aq, sa, s);
   if (rc != STQ1_OK) return rc;
-  return launch_product<kEpiI8F32>(down, s);
+  return launch_product<kEpiI8F32>(down, true, s);
 }

@@ -636,6 +636,7 @@ __device__ __forceinline__ void split_mmas(uint32_t tmem, int steps, uint32_t sb
 struct SplitArgs {
   DenseArgs p[2];
   int tiles0;                        // 128 x 128 tiles of the first product
+  int early;                         // B is not written by the kernel before: load it at once
 };
 
 // Each CTA of a cluster sums its piece of K in TMEM and lays the 128 x 128
@@ -677,34 +678,48 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   tc_fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(s_tmem));
-  griddep_wait();
-  griddep_launch_dependents();
-
   int tm, tn;
   dn_tile_pos(p, static_cast<int>(blockIdx.x) - (prob ? args.tiles0 : 0), tm, tn);
   const int k0 = static_cast<int>(static_cast<long long>(p.n_k) * piece / S);
   const int k1 = static_cast<int>(static_cast<long long>(p.n_k) * (piece + 1) / S);
   constexpr int kOutCols = GLU ? 64 : 128;
 
+  auto load_b = [&](int k, uint32_t dst, uint32_t b) {
+    if constexpr (GLU) {
+      // 64 gate rows and the 64 up rows of the same outputs
+      dn_load_operand<I8, BMN, 1>(dst, mb, k, tn * 64, 1, b);
+      dn_load_operand<I8, BMN, 1>(dst + kDnOperandBytes / 2, mb, k, static_cast<int>(p.N) + tn * 64, 1, b);
+    } else {
+      dn_load_operand<I8, BMN, 1>(dst, mb, k, tn * kDnRows, 2, b);
+    }
+  };
+  // With `early` the stages' first weights are on their way while the kernel
+  // before still runs (see dense_few_kernel for why that is sound).
+  const int ahead = args.early ? min(kSplitStages, k1 - k0) : 0;
+  if (warp == 4 && lane == 0) {
+    for (int i = 0; i < ahead; ++i) {
+      mbar_arrive_expect_tx(bar_full + 8 * i, p.a_bytes + kDnOperandBytes);
+      load_b(k0 + i, sbase + i * kDnStageBytes + kDnOperandBytes, bar_full + 8 * i);
+    }
+  }
+  __syncwarp();
+  griddep_wait();
+  griddep_launch_dependents();
+
   if (warp == 4) {
     if (lane == 0) {
       for (int k = k0; k < k1; ++k) {
         const uint32_t it = k - k0, s = it % kSplitStages, use = it / kSplitStages;
-        if (!mbar_wait_bounded(bar_empty + 8 * s, (use & 1) ^ 1)) break;
-        mbar_arrive_expect_tx(bar_full + 8 * s, p.a_bytes + kDnOperandBytes);
         const uint32_t dst = sbase + s * kDnStageBytes, b = bar_full + 8 * s;
+        if (k - k0 >= ahead) {
+          if (!mbar_wait_bounded(bar_empty + 8 * s, (use & 1) ^ 1)) break;
+          mbar_arrive_expect_tx(b, p.a_bytes + kDnOperandBytes);
+          load_b(k, dst + kDnOperandBytes, b);
+        }
         if (AMN || (DUAL && prob)) {
           dn_load_operand<I8, true, 1>(dst, ma, k, tm * kDnRows, 2, b);
         } else {
           dn_load<1>(dst, ma, k * (I8 ? 128 : 64), tm * kDnRows, b);      // one box of as many rows as a tile has
-        }
-        if constexpr (GLU) {
-          // 64 gate rows and the 64 up rows of the same outputs
-          dn_load_operand<I8, BMN, 1>(dst + kDnOperandBytes, mb, k, tn * 64, 1, b);
-          dn_load_operand<I8, BMN, 1>(dst + kDnOperandBytes + kDnOperandBytes / 2, mb, k,
-                                      static_cast<int>(p.N) + tn * 64, 1, b);
-        } else {
-          dn_load_operand<I8, BMN, 1>(dst + kDnOperandBytes, mb, k, tn * kDnRows, 2, b);
         }
       }
     }

@@ -61,6 +61,7 @@ SHAPES = [
     (65, 336, 88), (100, 2064, 1032), (128, 128, 64), (129, 272, 1024), (200, 1040, 1032), (256, 512, 256),
     (257, 528, 264), (300, 4096, 640), (513, 1040, 1032), (1000, 2048, 512), (1100, 528, 2056),
     (2600, 1072, 264), (2000, 2704, 72), (4000, 528, 136),
+    (1600, 2064, 1544), (2100, 2112, 1160), (700, 4096, 3600),
 ]
 
 
