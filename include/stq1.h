@@ -639,7 +639,7 @@ int stq1_i8_matmul(const int8_t* xq, const float* x_scales, const int8_t* wq, co
  *   (xq, sx) = stq1_quantize_i8(x);  y = stq1_i8_matmul(xq, gate/up) in fp32;
  *   act = stq1_swiglu(y);  (aq, sa) = stq1_quantize_i8(act);
  *   out = stq1_i8_matmul(aq, down) in fp32,
- * with the bits of that chain of calls; y and, for up to 16 tokens, the
+ * with the bits of that chain of calls; y and, with few tokens, the
  * activation's codes are never stored.
  *   x              device, [T, H] bf16 bits.
  *   gateup_q, gateup_scales  device, [N, H] codes (gate rows 0..N/2-1, up rows

@@ -159,6 +159,17 @@ long long single_tiles(const DenseProduct& d) {
   return (d.M + 127) / 128 * (((GLU ? 2 * d.N : d.N) + 127) / 128);
 }
 
+// Maps of the results: of d0, and of d1 (DUAL) or of the two halves of y.
+template <int EPI, bool DUAL>
+bool result_maps(const DenseProduct& d0, const DenseProduct& d1, CUtensorMap* o0, CUtensorMap* o1, CUtensorMap* o2) {
+  constexpr int kWidth = epi_glu(EPI) ? 64 : 128;
+  if (!make_result_map(o0, d0.out, EPI == kEpiI8F32, d0.M, d0.N, d0.N, kWidth)) return false;
+  if (DUAL) return make_result_map(o1, d1.out, false, d1.M, d1.N, d1.N, kWidth);
+  if (EPI != kEpiGlu || !d0.y) return true;
+  return make_result_map(o1, d0.y, false, d0.M, d0.N, 2 * d0.N, kWidth) &&
+         make_result_map(o2, d0.y + d0.N, false, d0.M, d0.N, 2 * d0.N, kWidth);
+}
+
 template <int EPI, bool AMN, bool BMN, bool DUAL>
 int launch_pairs(const DenseProduct& d0, const DenseProduct& d1, cudaStream_t s) {
   constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
@@ -175,12 +186,7 @@ int launch_pairs(const DenseProduct& d0, const DenseProduct& d1, cudaStream_t s)
     args.p[i] = tile_args<I8>(*d[i], tm, tn, kDnRows);
   }
   CUtensorMap o0{}, o1{}, o2{};
-  constexpr int kWidth = GLU ? 64 : 128;
-  if (!make_result_map(&o0, d0.out, EPI == kEpiI8F32, d0.M, d0.N, d0.N, kWidth)) return STQ1_ERR_CUDA;
-  if (DUAL && !make_result_map(&o1, d1.out, false, d1.M, d1.N, d1.N, kWidth)) return STQ1_ERR_CUDA;
-  if (EPI == kEpiGlu && d0.y && !(make_result_map(&o1, d0.y, false, d0.M, d0.N, 2 * d0.N, kWidth) &&
-                                  make_result_map(&o2, d0.y + d0.N, false, d0.M, d0.N, 2 * d0.N, kWidth)))
-    return STQ1_ERR_CUDA;
+  if (!result_maps<EPI, DUAL>(d0, d1, &o0, &o1, &o2)) return STQ1_ERR_CUDA;
   const int pairs = sm_count() / 2;
   int rest_tiles = static_cast<int>(tiles[0]);       // of the list's last part
   if (DUAL) {
@@ -236,9 +242,11 @@ int launch_split(const DenseProduct& d0, const DenseProduct& d1, int S, bool ear
     tiles += tm * tn;
     args.p[i] = tile_args<I8>(*d[i], tm, tn, i == 0 ? a_rows : kDnRows);
   }
+  CUtensorMap o0{}, o1{}, o2{};
+  if (S == 1 && !result_maps<EPI, DUAL>(d0, d1, &o0, &o1, &o2)) return STQ1_ERR_CUDA;
   auto launch = [&](auto kernel) {
     return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(S)), kSplitThreads,
-                              kSplitSmemBytes, s, static_cast<unsigned>(S), a0, b0, a1, b1, args);
+                              kSplitSmemBytes, s, static_cast<unsigned>(S), a0, b0, a1, b1, o0, o1, o2, args);
   };
   switch (S) {
     case 1: return launch(dense_split_kernel<EPI, AMN, BMN, DUAL, 1>);

@@ -124,6 +124,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
     for (int i = 0; i < p.n_slots && warp + kFewWarps * i < p.n_k; ++i) fetch(warp + kFewWarps * i, i);
   if (p.early) griddep_wait();
   griddep_launch_dependents();
+
   // ---- the tokens into shared memory ----
   const long long kbytes = p.K * ES;
   if constexpr (MADE) {

@@ -288,6 +288,90 @@ __device__ __forceinline__ void dn_store_plain(const uint32_t* w, uint32_t buf, 
   }
 }
 
+// One warp's block of finished sums: 32 rows by 64 columns of B at TMEM columns
+// t0 (32) and t1 (32 more; gated: the 32 up sums of the same outputs), from sums
+// to stored results.  scale: this lane's column scales of the two halves.
+// loaded() runs once the sums are in registers.  my0, my1: maps of the gate and
+// up halves of y.
+template <int EPI, typename F>
+__device__ __forceinline__ void dn_block_epilogue(uint32_t t0, uint32_t t1, float sx, const float (&scale)[2],
+                                                  const DenseArgs& p, const CUtensorMap* mo, const CUtensorMap* my0,
+                                                  const CUtensorMap* my1, uint32_t buf, long long row0, long long col0,
+                                                  F&& loaded) {
+  constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
+  constexpr int ES = EPI == kEpiI8F32 ? 4 : 2;
+  const bool copies = p.N % (16 / ES) == 0, in = row0 < p.M && col0 < p.N;
+  const int x = static_cast<int>(col0), y = static_cast<int>(row0);
+  uint32_t v0[32], v1[32];
+  STQ1_TMEM_LD32(t0, v0);
+  STQ1_TMEM_LD32(t1, v1);
+  tmem_wait_ld();
+  loaded();
+  if (!in) return;
+  auto sum0 = [&](int j) { return dn_sum<I8>(v0[j], sx, I8 ? __shfl_sync(0xffffffffu, scale[0], j) : 0.f); };
+  auto sum1 = [&](int j) { return dn_sum<I8>(v1[j], sx, I8 ? __shfl_sync(0xffffffffu, scale[1], j) : 0.f); };
+  if constexpr (GLU) {
+    // Rows and columns past the edges hold zeros or anything at all, which the
+    // activation would take the long way round; they count as one instead.
+    const bool row_in = row0 + (threadIdx.x & 31) < p.M;
+    const int cols = static_cast<int>(min(32LL, p.N - col0));
+    uint32_t act[16], kg[16], ku[16];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float gv[16], uv[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float gs = sum0(16 * c + j), us = sum1(16 * c + j);
+        const bool is = row_in && 16 * c + j < cols;
+        gv[j] = is ? gs : 1.f;
+        uv[j] = is ? us : 1.f;
+      }
+      swiglu_bf16_pack<16>(gv, uv, act + 8 * c);
+      if constexpr (EPI == kEpiGlu) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          kg[8 * c + j / 2] = bf16_bits_rn(gv[j]) | (bf16_bits_rn(gv[j + 1]) << 16);
+          ku[8 * c + j / 2] = bf16_bits_rn(uv[j]) | (bf16_bits_rn(uv[j + 1]) << 16);
+        }
+      }
+    }
+    // N is a multiple of 8: rows are always whole pieces of 16 bytes
+    dn_store_copy<16>(act, buf, mo, x, y);
+    if (EPI == kEpiGlu && p.y) {
+      dn_store_copy<16>(kg, buf, my0, x, y);
+      dn_store_copy<16>(ku, buf, my1, x, y);
+    }
+  } else if constexpr (ES == 4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(h ? sum1(j) : sum0(j));
+      if (col0 + 32 * h >= p.N) continue;
+      if (copies) dn_store_copy<32>(w, buf, mo, x + 32 * h, y);
+      else dn_store_plain<4, 32>(w, buf, p.out, row0, p.M, p.N, col0 + 32 * h, p.N);
+    }
+  } else {
+    uint32_t w[32];
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      w[j / 2] = bf16_bits_rn(sum0(j)) | (bf16_bits_rn(sum0(j + 1)) << 16);
+      w[16 + j / 2] = bf16_bits_rn(sum1(j)) | (bf16_bits_rn(sum1(j + 1)) << 16);
+    }
+    if (copies) dn_store_copy<32>(w, buf, mo, x, y);
+    else dn_store_plain<2, 32>(w, buf, p.out, row0, p.M, p.N, col0, p.N);
+  }
+}
+// The scales of a block's columns: of B's rows col0 + lane and, for the second
+// half, 32 further (gated: of the up row of the same output).
+template <bool GLU>
+__device__ __forceinline__ void dn_block_scales(const DenseArgs& p, long long col0, float (&scale)[2]) {
+  const long long c = col0 + (threadIdx.x & 31);
+  scale[0] = c < p.N ? p.sw[c] : 0.f;
+  if (GLU) scale[1] = c < p.N ? p.sw[p.N + c] : 0.f;
+  else scale[1] = c + 32 < p.N ? p.sw[c + 32] : 0.f;
+}
+
 // A unit of the pair kernel's work: which product, the tile's place, and
 // whether it is a whole tile or one half of its columns.
 struct PairUnit {
@@ -413,7 +497,6 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   griddep_wait();
   griddep_launch_dependents();
 
-
   if (warp == kPairWarpA || warp == kPairWarpB) {
     // ---- producers: this CTA's 128 rows of A and 128 or 64 rows of B per step ----
     // A wait that runs out ends the role; it started after the last copy was
@@ -479,17 +562,14 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
     const uint32_t buf0 = sbase + kPairOffStage + warp * 4096;
     const uint32_t acc_empty0 = dn_mapa(bar_acc_empty, 0);
-    constexpr int ES = EPI == kEpiI8F32 ? 4 : 2;
     constexpr int kMine = 4 / kPairSides;            // column blocks of a whole tile that are this warp's
     uint32_t t = 0;
     PairUnit un;
     for (; pair_unit<DUAL>(args, static_cast<int>(t), un); ++t) {
       const uint32_t buf = t & 1, use = t >> 1;
       const DenseArgs& p = args.p[un.prob];
-      const bool copies = p.N % (16 / ES) == 0;
       const CUtensorMap* mo = DUAL && un.prob ? &map_o1 : &map_o;
       const long long row0 = un.tm * 256LL + rank * kDnRows + 32 * quad;
-      const bool rows_in = row0 < p.M;
       const float sx = I8 && row0 + lane < p.M ? p.sx[row0 + lane] : 0.f;
       // blocks of 64 columns of B: four of a whole tile, two of a half
       const int blocks = un.half < 0 ? 4 : 2;
@@ -501,15 +581,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       float scale[kMine][2] = {};
       if constexpr (I8) {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const long long c = first_col(side + i * kPairSides) + lane;
-          if (GLU) {
-            if (c < p.N) scale[i][0] = p.sw[c], scale[i][1] = p.sw[p.N + c];
-          } else {
-            if (c < p.N) scale[i][0] = p.sw[c];
-            if (c + 32 < p.N) scale[i][1] = p.sw[c + 32];
-          }
-        }
+        for (int i = 0; i < kMine; ++i) dn_block_scales<GLU>(p, first_col(side + i * kPairSides), scale[i]);
       }
       if (!mbar_wait_bounded(bar_acc_full + 8 * buf, use & 1)) break;
       tc_fence_after();
@@ -525,65 +597,11 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         if (blk >= blocks) break;
         const bool last = blk + kPairSides >= blocks;
         const long long col0 = first_col(blk);
-        const bool in = rows_in && col0 < p.N;
-        const int x = static_cast<int>(col0), y = static_cast<int>(row0);
-        uint32_t v0[32], v1[32];
-        // gated: 32 gate sums and, `up` further, the 32 up sums of the same outputs; else 64 sums
-        STQ1_TMEM_LD32(acc + (GLU ? 32 : 64) * blk, v0);
-        STQ1_TMEM_LD32(acc + (GLU ? (un.half < 0 ? 128 : 64) + 32 * blk : 64 * blk + 32), v1);
-        tmem_wait_ld();
-        if (last) release();
-        auto sum0 = [&](int j) { return dn_sum<I8>(v0[j], sx, I8 ? __shfl_sync(0xffffffffu, scale[i][0], j) : 0.f); };
-        auto sum1 = [&](int j) { return dn_sum<I8>(v1[j], sx, I8 ? __shfl_sync(0xffffffffu, scale[i][1], j) : 0.f); };
-        if constexpr (GLU) {
-          uint32_t act[16], kg[16], ku[16];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float gv[16], uv[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              gv[j] = sum0(16 * c + j);
-              uv[j] = sum1(16 * c + j);
-            }
-            swiglu_bf16_pack<16>(gv, uv, act + 8 * c);
-            if constexpr (EPI == kEpiGlu) {
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                kg[8 * c + j / 2] = bf16_bits_rn(gv[j]) | (bf16_bits_rn(gv[j + 1]) << 16);
-                ku[8 * c + j / 2] = bf16_bits_rn(uv[j]) | (bf16_bits_rn(uv[j + 1]) << 16);
-              }
-            }
-          }
-          // N is a multiple of 8: rows are always whole pieces of 16 bytes
-          if (in) {
-            dn_store_copy<16>(act, buf0, mo, x, y);
-            if (EPI == kEpiGlu && p.y) {
-              dn_store_copy<16>(kg, buf0, &map_o1, x, y);
-              dn_store_copy<16>(ku, buf0, &map_o2, x, y);
-            }
-          }
-        } else if constexpr (ES == 4) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(h ? sum1(j) : sum0(j));
-            if (!rows_in || col0 + 32 * h >= p.N) continue;
-            if (copies) dn_store_copy<32>(w, buf0, mo, x + 32 * h, y);
-            else dn_store_plain<4, 32>(w, buf0, p.out, row0, p.M, p.N, col0 + 32 * h, p.N);
-          }
-        } else {
-          uint32_t w[32];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            w[j / 2] = bf16_bits_rn(sum0(j)) | (bf16_bits_rn(sum0(j + 1)) << 16);
-            w[16 + j / 2] = bf16_bits_rn(sum1(j)) | (bf16_bits_rn(sum1(j + 1)) << 16);
-          }
-          if (in) {
-            if (copies) dn_store_copy<32>(w, buf0, mo, x, y);
-            else dn_store_plain<2, 32>(w, buf0, p.out, row0, p.M, p.N, col0, p.N);
-          }
-        }
+        dn_block_epilogue<EPI>(acc + (GLU ? 32 : 64) * blk,
+                               acc + (GLU ? (un.half < 0 ? 128 : 64) + 32 * blk : 64 * blk + 32), sx, scale[i], p, mo,
+                               &map_o1, &map_o2, buf0, row0, col0, [&]() {
+                                 if (last) release();
+                               });
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -642,12 +660,14 @@ struct SplitArgs {
 // Each CTA of a cluster sums its piece of K in TMEM and lays the 128 x 128
 // sums into its shared memory; each then adds up its share of the rows over
 // all pieces, in the order of the pieces, and stores them: the result does not
-// depend on which CTA comes first.  DUAL: as in the pair kernel.
+// depend on which CTA comes first.  With one piece the sums go to the result
+// as in the pair kernel.  DUAL, map_o...: as there.
 template <int EPI, bool AMN, bool BMN, bool DUAL, int S>
 __global__ void __launch_bounds__(kSplitThreads, 1)
 dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b1,
-                   const __grid_constant__ SplitArgs args) {
+                   const __grid_constant__ CUtensorMap map_o, const __grid_constant__ CUtensorMap map_o1,
+                   const __grid_constant__ CUtensorMap map_o2, const __grid_constant__ SplitArgs args) {
   constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const uint32_t sraw = smem_u32(smem_raw);
@@ -729,7 +749,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       else split_mmas<I8, AMN, BMN>(tmem, k1 - k0, sbase, bar_full, bar_empty);
       tc_commit(bar_acc);                            // all MMAs so far, in the error case too
     }
-  } else if (warp < 4) {
+  } else if (S > 1 && warp < 4) {
     // the sums to shared memory (the stages are free once the last MMA is done); an empty piece sums to zero
     mbar_wait_bounded(bar_acc, 0);
     tc_fence_after();
@@ -749,10 +769,34 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       }
     }
   }
-  tc_fence_before();
   __syncwarp();
-  if constexpr (S > 1) cluster_sync_all();           // every piece lies in shared memory
-  else __syncthreads();
+  if constexpr (S == 1) {
+    // the whole of K: every warp takes 32 rows and half of the columns, from TMEM to the result
+    // (by way of whole rows in shared memory, as with S > 1, 805 tokens by [544, 208] took 5.3 us, gated 7.0)
+    const long long row0 = static_cast<long long>(tm) * kDnRows + 32 * (warp & 3);
+    const long long col0 = static_cast<long long>(tn) * kOutCols + kOutCols / 2 * (warp >> 2);
+    const float sx = I8 && row0 + lane < p.M ? p.sx[row0 + lane] : 0.f;
+    float scale[2] = {};
+    if constexpr (I8) dn_block_scales<GLU>(p, col0, scale);
+    if (mbar_wait_bounded(bar_acc, 0)) {
+      tc_fence_after();
+      const uint32_t acc = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+      const int h = warp >> 2;
+      dn_block_epilogue<EPI>(acc + (GLU ? 32 * h : 64 * h), acc + (GLU ? 64 + 32 * h : 64 * h + 32), sx, scale, p,
+                             DUAL && prob ? &map_o1 : &map_o, &map_o1, &map_o2, sbase + warp * 4096, row0, col0, []() {});
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+      tc_fence_after();
+      dn_tmem_dealloc<1>(tmem, 128);
+    }
+    return;
+  }
+  tc_fence_before();
+  cluster_sync_all();                                // every piece lies in shared memory
   if (warp == 5) {
     tc_fence_after();
     dn_tmem_dealloc<1>(tmem, 128);
@@ -760,7 +804,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
 
   // this CTA's rows: piece, piece + S, ... ; a warp takes kRows of them at a time, so that their reads overlap, a
   // lane four sums of each (or two gate/up pairs)
-  constexpr int kRows = S >= 8 ? 1 : (S == 1 ? 4 : 2);
+  constexpr int kRows = S >= 8 ? 1 : 2;
   constexpr int kWarps = kSplitThreads / 32;
   const long long m0 = static_cast<long long>(tm) * kDnRows;
   const long long n0 = static_cast<long long>(tn) * kOutCols;
@@ -784,7 +828,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       const uint32_t at = sbase + r * (kSplitPitch * 4);
 #pragma unroll
       for (int q = 0; q < S; ++q) {
-        const uint32_t src = S > 1 ? dn_mapa(at, q) : at;
+        const uint32_t src = dn_mapa(at, q);
         uint32_t(&o)[4] = w[j][q];
         if constexpr (GLU) {
           asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(o[0]), "=r"(o[1]) : "r"(src + 8 * lane) : "memory");
@@ -851,10 +895,8 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       }
     }
   }
-  if constexpr (S > 1) {
-    __syncwarp();
-    cluster_sync_all();                              // a peer may still read this CTA's piece
-  }
+  __syncwarp();
+  cluster_sync_all();                                // a peer may still read this CTA's piece
 }
 
 }  // namespace stq1
