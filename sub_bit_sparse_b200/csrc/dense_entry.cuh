@@ -213,16 +213,22 @@ int launch_pairs(const DenseProduct& d0, const DenseProduct& d1, cudaStream_t s)
                     kPairSmemBytes, s, a0, b0, a1, b1, o0, o1, o2, args);
 }
 
-// Pieces of K for so many tiles of n_k steps: as many as run at once, two steps
-// each at least.  (Clusters of eight for 17 tiles, of which the GPCs hold 16 at a
-// time: 9.3 us for [2053, 2048] weights and 77 tokens; clusters of four: 5.6.)
-int split_pieces(long long tiles, int n_k) {
+// Pieces of K for so many tiles of n_k steps, `least` steps each at least: as
+// many as run at once.  (Clusters of eight for 17 tiles, of which the GPCs hold 16
+// at a time: 9.3 us for [2053, 2048] weights and 77 tokens; clusters of four: 5.6.)
+int split_pieces(long long tiles, int n_k, int least) {
   const int dev = current_device();
   int S = 1;
   for (int i = 1; i <= 3; ++i)
-    if (dev >= 0 && tiles <= g_max_clusters[dev][i].load(std::memory_order_relaxed) && (2 << i) <= n_k) S = 1 << i;
+    if (dev >= 0 && tiles <= g_max_clusters[dev][i].load(std::memory_order_relaxed) && (least << i) <= n_k) S = 1 << i;
   return S;
 }
+// Joining the pieces costs about four steps, less where there are few rows to
+// join or where it spreads the activation's work (int8, 120 tokens by [1024, K]:
+// 4 steps 4.3 us whole and 5.0 in two pieces, 8 steps 5.3 and 5.4, 16 steps 7.0
+// and 6.4; 32 tokens, 8 steps 4.6 and 4.2; gated, 120 tokens, 8 steps 7.2 and 6.4
+// in four).
+int least_steps(long long M, bool glu) { return glu || M <= 32 ? 2 : 4; }
 
 template <int EPI, bool AMN, bool BMN, bool DUAL>
 int launch_split(const DenseProduct& d0, const DenseProduct& d1, int S, bool early, cudaStream_t s) {
@@ -265,7 +271,8 @@ int launch_tiles(const DenseProduct& d, bool early, cudaStream_t s) {
   int rc = ensure_dense_configured();
   if (rc != STQ1_OK) return rc;
   if (single_tiles<epi_glu(EPI)>(d) > sm_count()) return launch_pairs<EPI, AMN, BMN, false>(d, d, s);
-  return launch_split<EPI, AMN, BMN, false>(d, d, split_pieces(single_tiles<epi_glu(EPI)>(d), k_steps(d.K, epi_i8(EPI))), early, s);
+  return launch_split<EPI, AMN, BMN, false>(d, d, split_pieces(single_tiles<epi_glu(EPI)>(d), k_steps(d.K, epi_i8(EPI)),
+                                                               least_steps(d.M, epi_glu(EPI))), early, s);
 }
 
 // How a product with few tokens is laid out: outputs per CTA so that every SM
@@ -449,7 +456,7 @@ extern "C" int stq1_glu_backward(const uint16_t* dact, const uint16_t* y, const 
   // as for both in any case
   const long long tx = single_tiles<false>(px), tw = single_tiles<false>(pw);
   if (tx + tw <= sm_count()) {
-    const int S = split_pieces(tx + tw, std::max(k_steps(N, false), k_steps(T, false)));
+    const int S = split_pieces(tx + tw, std::max(k_steps(N, false), k_steps(T, false)), 4);
     if (dx && dW) return launch_split<kEpiBf16, false, true, true>(px, pw, S, false, s);
     return dx ? launch_split<kEpiBf16, false, true, false>(px, px, S, false, s)
               : launch_split<kEpiBf16, true, true, false>(pw, pw, S, false, s);

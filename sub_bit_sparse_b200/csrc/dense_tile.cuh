@@ -243,11 +243,14 @@ __device__ __forceinline__ void dn_block_to_smem(const uint32_t* w, uint32_t buf
                  "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
                  : "memory");
 }
-template <int WORDS>
+// REUSE: an earlier copy may still be reading the buffer.
+template <int WORDS, bool REUSE>
 __device__ __forceinline__ void dn_store_copy(const uint32_t* w, uint32_t buf, const CUtensorMap* map, int x, int y) {
   const int lane = threadIdx.x & 31;
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  __syncwarp();
+  if constexpr (REUSE) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+  }
   dn_block_to_smem<WORDS>(w, buf);
   fence_proxy_async_smem();
   __syncwarp();
@@ -292,8 +295,9 @@ __device__ __forceinline__ void dn_store_plain(const uint32_t* w, uint32_t buf, 
 // t0 (32) and t1 (32 more; gated: the 32 up sums of the same outputs), from sums
 // to stored results.  scale: this lane's column scales of the two halves.
 // loaded() runs once the sums are in registers.  my0, my1: maps of the gate and
-// up halves of y.
-template <int EPI, typename F>
+// up halves of y.  REUSE: `buf` is one buffer for all of the warp's blocks; else
+// there are three, used once.
+template <int EPI, bool REUSE, typename F>
 __device__ __forceinline__ void dn_block_epilogue(uint32_t t0, uint32_t t1, float sx, const float (&scale)[2],
                                                   const DenseArgs& p, const CUtensorMap* mo, const CUtensorMap* my0,
                                                   const CUtensorMap* my1, uint32_t buf, long long row0, long long col0,
@@ -336,10 +340,10 @@ __device__ __forceinline__ void dn_block_epilogue(uint32_t t0, uint32_t t1, floa
       }
     }
     // N is a multiple of 8: rows are always whole pieces of 16 bytes
-    dn_store_copy<16>(act, buf, mo, x, y);
+    dn_store_copy<16, REUSE>(act, buf, mo, x, y);
     if (EPI == kEpiGlu && p.y) {
-      dn_store_copy<16>(kg, buf, my0, x, y);
-      dn_store_copy<16>(ku, buf, my1, x, y);
+      dn_store_copy<16, REUSE>(kg, REUSE ? buf : buf + 4096, my0, x, y);
+      dn_store_copy<16, REUSE>(ku, REUSE ? buf : buf + 8192, my1, x, y);
     }
   } else if constexpr (ES == 4) {
 #pragma unroll
@@ -348,7 +352,7 @@ __device__ __forceinline__ void dn_block_epilogue(uint32_t t0, uint32_t t1, floa
 #pragma unroll
       for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(h ? sum1(j) : sum0(j));
       if (col0 + 32 * h >= p.N) continue;
-      if (copies) dn_store_copy<32>(w, buf, mo, x + 32 * h, y);
+      if (copies) dn_store_copy<32, REUSE>(w, REUSE ? buf : buf + 4096 * h, mo, x + 32 * h, y);
       else dn_store_plain<4, 32>(w, buf, p.out, row0, p.M, p.N, col0 + 32 * h, p.N);
     }
   } else {
@@ -358,7 +362,7 @@ __device__ __forceinline__ void dn_block_epilogue(uint32_t t0, uint32_t t1, floa
       w[j / 2] = bf16_bits_rn(sum0(j)) | (bf16_bits_rn(sum0(j + 1)) << 16);
       w[16 + j / 2] = bf16_bits_rn(sum1(j)) | (bf16_bits_rn(sum1(j + 1)) << 16);
     }
-    if (copies) dn_store_copy<32>(w, buf, mo, x, y);
+    if (copies) dn_store_copy<32, REUSE>(w, buf, mo, x, y);
     else dn_store_plain<2, 32>(w, buf, p.out, row0, p.M, p.N, col0, p.N);
   }
 }
@@ -597,7 +601,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         if (blk >= blocks) break;
         const bool last = blk + kPairSides >= blocks;
         const long long col0 = first_col(blk);
-        dn_block_epilogue<EPI>(acc + (GLU ? 32 : 64) * blk,
+        dn_block_epilogue<EPI, true>(acc + (GLU ? 32 : 64) * blk,
                                acc + (GLU ? (un.half < 0 ? 128 : 64) + 32 * blk : 64 * blk + 32), sx, scale[i], p, mo,
                                &map_o1, &map_o2, buf0, row0, col0, [&]() {
                                  if (last) release();
@@ -633,6 +637,7 @@ constexpr int kSplitPitch = 132;                    // words per row of a finish
 constexpr int kSplitOffBar = kSplitStages * kDnStageBytes;
 constexpr int kSplitSmemBytes = 1024 + kSplitOffBar + 256;
 static_assert(kDnRows * kSplitPitch * 4 <= kSplitOffBar, "a finished piece takes the place of the stages");
+static_assert(kSplitThreads / 32 * 12288 <= kSplitOffBar, "and so do the blocks of results");
 
 template <bool I8, bool AMN, bool BMN>
 __device__ __forceinline__ void split_mmas(uint32_t tmem, int steps, uint32_t sbase, uint32_t bar_full,
@@ -782,8 +787,8 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
       const int h = warp >> 2;
-      dn_block_epilogue<EPI>(acc + (GLU ? 32 * h : 64 * h), acc + (GLU ? 64 + 32 * h : 64 * h + 32), sx, scale, p,
-                             DUAL && prob ? &map_o1 : &map_o, &map_o1, &map_o2, sbase + warp * 4096, row0, col0, []() {});
+      dn_block_epilogue<EPI, false>(acc + (GLU ? 32 * h : 64 * h), acc + (GLU ? 64 + 32 * h : 64 * h + 32), sx, scale, p,
+                             DUAL && prob ? &map_o1 : &map_o, &map_o1, &map_o2, sbase + warp * 12288, row0, col0, []() {});
       if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncwarp();
