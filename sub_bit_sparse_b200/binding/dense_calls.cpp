@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -88,18 +89,23 @@ const at::Tensor& operand(PyObject* o, at::ScalarType type, std::initializer_lis
   return t;
 }
 
+// A new tensor, straight from the caching allocator (0.3 us a tensor less than
+// by way of the dispatcher).
+at::Tensor made(std::initializer_list<int64_t> shape, at::ScalarType type, const at::Tensor& like) {
+  return at::detail::empty_cuda(at::IntArrayRef(shape.begin(), shape.size()), type, like.device(), std::nullopt);
+}
+
 // An output: the caller's, checked, or a new one.
 at::Tensor output(PyObject* o, at::ScalarType type, std::initializer_list<int64_t> shape, const at::Tensor& like,
                   const char* name) {
   if (o != Py_None) return operand(o, type, shape, like.get_device(), name);
-  return at::empty(at::IntArrayRef(shape.begin(), shape.size()), at::TensorOptions().dtype(type).device(like.device()));
+  return made(shape, type, like);
 }
 
 // The caller's workspace, or one of this call's own: calls on two streams, or
 // captured in two graphs, then never share one.
 at::Tensor scratch(PyObject* o, int64_t bytes, const at::Tensor& like) {
-  if (o == Py_None)
-    return at::empty({bytes > 16 ? bytes : 16}, at::TensorOptions().dtype(at::kByte).device(like.device()));
+  if (o == Py_None) return made({bytes > 16 ? bytes : 16}, at::kByte, like);
   const at::Tensor& t = tensor(o, at::kByte, "ws");
   if (t.get_device() != like.get_device()) throw Refusal{PyExc_ValueError, "ws must be on the operands' device"};
   return t;

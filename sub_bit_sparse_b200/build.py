@@ -83,7 +83,8 @@ def build_binding(verbose: bool = False, force: bool = False) -> str:
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *[a for p in include_paths() for a in ("-isystem", p)], "-isystem", sysconfig.get_paths()["include"],
           "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
-          *["-L" + p for p in library_paths()], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ltorch"], verbose)
+          *["-L" + p for p in library_paths()], "-lc10", "-lc10_cuda", "-ltorch_cpu",
+          "-ltorch_cuda", "-ltorch_python", "-ltorch"], verbose)
     os.replace(tmp, BINDING)
     return BINDING
 

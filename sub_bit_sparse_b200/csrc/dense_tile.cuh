@@ -262,32 +262,31 @@ __device__ __forceinline__ void dn_store_copy(const uint32_t* w, uint32_t buf, c
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
 }
-// The same for rows that tensor copies cannot address (a row's bytes are no
-// multiple of 16): element by element.
-template <int ES, int WORDS>
+// The same (blocks of 32 words a row) for rows that tensor copies cannot
+// address, because a row's bytes are no multiple of 16: a row at a time, a lane
+// per word.
+template <int ES>
 __device__ __forceinline__ void dn_store_plain(const uint32_t* w, uint32_t buf, void* out, long long row0,
                                                long long rows, long long ld, long long col0, long long cols) {
   const int lane = threadIdx.x & 31;
-  constexpr int kPer = 4 / ES, kPieces = WORDS / 4;
   __syncwarp();                                     // the previous block's reads are done
-  dn_block_to_smem<WORDS>(w, buf);
+  dn_block_to_smem<32>(w, buf);
   __syncwarp();
-  char* base = static_cast<char*>(out);
-  const int piece = lane % kPieces;
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int r = (32 / kPieces) * i + lane / kPieces;
-    if (row0 + r >= rows) continue;
-    const uint4 v = lds_v4(buf + dn_place<WORDS>(r, piece));
-    const long long c = col0 + piece * 4 * kPer;
-    char* dst = base + ((row0 + r) * ld + c) * ES;
-    const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4 * kPer; ++j)
-      if (c + j < cols) {
-        if constexpr (ES == 4) reinterpret_cast<uint32_t*>(dst)[j] = e[j];
-        else reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>(e[j >> 1] >> (16 * (j & 1)));
-      }
+  const int n = static_cast<int>(min(32LL, rows - row0));
+  const long long c = col0 + lane * (4 / ES);
+  char* dst = static_cast<char*>(out) + (row0 * ld + c) * ES;
+#pragma unroll 4
+  for (int r = 0; r < n; ++r, dst += ld * ES) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(buf + dn_place<32>(r, lane >> 2) + 4 * (lane & 3)));
+    if constexpr (ES == 4) {
+      if (c < cols) *reinterpret_cast<uint32_t*>(dst) = v;
+    } else if ((ld & 1) == 0) {
+      if (c < cols) *reinterpret_cast<uint32_t*>(dst) = v;       // an even row length: both values or neither
+    } else {
+      if (c < cols) reinterpret_cast<uint16_t*>(dst)[0] = static_cast<uint16_t>(v);
+      if (c + 1 < cols) reinterpret_cast<uint16_t*>(dst)[1] = static_cast<uint16_t>(v >> 16);
+    }
   }
 }
 
@@ -353,7 +352,7 @@ __device__ __forceinline__ void dn_block_epilogue(uint32_t t0, uint32_t t1, floa
       for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(h ? sum1(j) : sum0(j));
       if (col0 + 32 * h >= p.N) continue;
       if (copies) dn_store_copy<32, REUSE>(w, REUSE ? buf : buf + 4096 * h, mo, x + 32 * h, y);
-      else dn_store_plain<4, 32>(w, buf, p.out, row0, p.M, p.N, col0 + 32 * h, p.N);
+      else dn_store_plain<4>(w, buf, p.out, row0, p.M, p.N, col0 + 32 * h, p.N);
     }
   } else {
     uint32_t w[32];
@@ -363,7 +362,7 @@ __device__ __forceinline__ void dn_block_epilogue(uint32_t t0, uint32_t t1, floa
       w[16 + j / 2] = bf16_bits_rn(sum1(j)) | (bf16_bits_rn(sum1(j + 1)) << 16);
     }
     if (copies) dn_store_copy<32, REUSE>(w, buf, mo, x, y);
-    else dn_store_plain<2, 32>(w, buf, p.out, row0, p.M, p.N, col0, p.N);
+    else dn_store_plain<2>(w, buf, p.out, row0, p.M, p.N, col0, p.N);
   }
 }
 // The scales of a block's columns: of B's rows col0 + lane and, for the second
