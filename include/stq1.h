@@ -589,6 +589,7 @@ int stq1_mix_allocate(const double* err_low, const double* err_high, const doubl
  * Two calls with the same inputs and sizes give the same bits (sums that are
  * split are joined in a fixed order), and a row's results do not depend on what
  * the other rows hold.  Nothing but the outputs and the workspace is written.
+ * Outputs and workspace must overlap neither one another nor the inputs.
  * No index is taken from device memory, so the debug build checks nothing more
  * here.  The kernel is chosen by the sizes: up to 16 tokens a streaming kernel
  * (mma.sync), else tensor-core tiles (tcgen05).

@@ -223,12 +223,14 @@ int split_pieces(long long tiles, int n_k, int least) {
     if (dev >= 0 && tiles <= g_max_clusters[dev][i].load(std::memory_order_relaxed) && (least << i) <= n_k) S = 1 << i;
   return S;
 }
-// Joining the pieces costs about four steps, less where there are few rows to
-// join or where it spreads the activation's work (int8, 120 tokens by [1024, K]:
-// 4 steps 4.3 us whole and 5.0 in two pieces, 8 steps 5.3 and 5.4, 16 steps 7.0
-// and 6.4; 32 tokens, 8 steps 4.6 and 4.2; gated, 120 tokens, 8 steps 7.2 and 6.4
-// in four).
-int least_steps(long long M, bool glu) { return glu || M <= 32 ? 2 : 4; }
+// Joining the pieces costs about four steps whatever their number, less where
+// there are few rows to join or where it spreads the activation's work: int8, 120
+// tokens by [1024, K], whole / two / four / eight pieces: 4 steps 4.3, 5.0, 5.1,
+// 5.1 us, 8 steps 5.3, 5.5, 5.4, 5.5, 10 steps 5.8, 5.8, 5.6, 5.5, 16 steps 7.1, 6.5,
+// 5.8, 5.7; 64 tokens, 8 steps 4.9, 4.6, 4.4, 4.5; gated, 120 tokens, 8 steps 7.2
+// whole and 6.4 in four.  So short products of many rows stay whole, and else a
+// piece has two steps.
+int least_steps(long long M, int n_k, bool glu) { return glu || M <= 64 || n_k >= 10 ? 2 : n_k; }
 
 template <int EPI, bool AMN, bool BMN, bool DUAL>
 int launch_split(const DenseProduct& d0, const DenseProduct& d1, int S, bool early, cudaStream_t s) {
@@ -272,7 +274,7 @@ int launch_tiles(const DenseProduct& d, bool early, cudaStream_t s) {
   if (rc != STQ1_OK) return rc;
   if (single_tiles<epi_glu(EPI)>(d) > sm_count()) return launch_pairs<EPI, AMN, BMN, false>(d, d, s);
   return launch_split<EPI, AMN, BMN, false>(d, d, split_pieces(single_tiles<epi_glu(EPI)>(d), k_steps(d.K, epi_i8(EPI)),
-                                                               least_steps(d.M, epi_glu(EPI))), early, s);
+                                                               least_steps(d.M, k_steps(d.K, epi_i8(EPI)), epi_glu(EPI))), early, s);
 }
 
 // How a product with few tokens is laid out: outputs per CTA so that every SM
