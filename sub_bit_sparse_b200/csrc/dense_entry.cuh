@@ -51,7 +51,8 @@ bool make_result_map(CUtensorMap* map, void* base, bool f32, long long rows, lon
 }
 
 std::atomic<bool> g_dense_configured[kMaxDevices];
-constexpr int kFewAllSmem = 232448;
+constexpr int kFewAllSmem = 232448;        // of one CTA on an SM
+constexpr int kFewHalfSmem = 233472 / 2 - 1024;   // of each of two (an SM has 228 KB and keeps 1 KB per CTA)
 template <int EPI, bool MADE, int MT, int NT>
 bool few_config_one() {
   return cudaFuncSetAttribute(dense_few_kernel<EPI, MADE, MT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -278,27 +279,55 @@ int launch_tiles(const DenseProduct& d, bool early, cudaStream_t s) {
 }
 
 // How a product with few tokens is laid out: outputs per CTA so that every SM
-// has one CTA's share, and as many steps in flight per warp as fit.
+// has one CTA's share (or several in even rounds), and as many steps in flight
+// per warp as fit.
 struct FewPlan {
   int rows, pad, n_k, n_slots;
   size_t smem;
 };
-bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu) {
+// false: the tile kernels take it.  early: the weights are asked for before the
+// kernel before has run.  The rules, each with both sides measured:
+// - a CTA whose weights are read quickly (up to 256 KB) leaves room for a second
+//   one on its SM, so that the next launch starts beside it: int8 [4096, 7168] at
+//   one token 5.9 -> 5.3 us, gated [2048, 7168] 8.7 -> 7.7; with 400 KB, gated
+//   [4096, 7168], the steps in flight count for more: 12.2 and 12.7.
+// - early, no more than four steps per warp: a deeper queue of copies holds up
+//   the tokens' codes (8-bit layer of [4096, 7168], 8 tokens 16.5 -> 15.8 us).
+// - more outputs than one round of CTAs, and single tiles that run at once: the
+//   tiles (int8 [16384, 4096]: 15.7 us and 14.3 on tiles at one token, 20.1 and
+//   14.7 at 16), except where the rounds overlap because two CTAs fit an SM
+//   ([11008, 4096] at one token 9.8 and 11.9), and in the 8-bit layer up to two
+//   tokens, where it saves the launch for the codes (25.6 us against 27.8 for a
+//   layer of [16384, 4096]).
+// - more tiles than that: int8 above 8 tokens on tiles ([65536, 2048], 12 tokens:
+//   42.8 and 36.2 us; 8 tokens: 36.4 and 37.5), the gated form here ([28672, 4096],
+//   12 tokens: 52.0 and 63.0).
+bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu, bool early) {
   if (T > kFewMaxTokens) return false;
   const int sms = sm_count(), unit = glu ? 8 : 16;         // the gate rows end on a whole swizzle atom
-  f->rows = static_cast<int>(std::min<long long>(glu ? 32 : 64, (N + sms - 1) / sms));
+  const long long round_rows = sms * (glu ? 32LL : 64LL), rounds = (N + round_rows - 1) / round_rows;
+  f->rows = static_cast<int>((N + sms * rounds - 1) / (sms * rounds));
   f->pad = (f->rows + unit - 1) / unit * unit * (glu ? 2 : 1);
   f->n_k = static_cast<int>((kbytes + kDnStepBytes - 1) / kDnStepBytes);
   const long long x = few_pitch(f->n_k) * T;
   const long long per_warp = (f->n_k + kFewWarps - 1) / kFewWarps;
-  const long long round = static_cast<long long>(f->pad) * kDnStepBytes * kFewWarps;     // one slot per warp
-  const long long slots = std::min<long long>(std::min<long long>((kFewAllSmem - 1024 - kFewHead - x) / round, per_warp),
-                                              kFewMaxSlots);
-  if (slots < 1 || (slots < 2 && per_warp > 1)) return false;
+  const long long step = static_cast<long long>(f->pad) * kDnStepBytes * kFewWarps;      // one slot per warp
+  auto fit = [&](long long smem) {
+    return std::min<long long>(std::min<long long>((smem - 1024 - kFewHead - x) / step, per_warp), kFewMaxSlots);
+  };
+  const long long half = fit(kFewHalfSmem);
+  const bool two = f->rows * (glu ? 2 : 1) * kbytes <= 256 * 1024 && half >= std::min<long long>(2, per_warp);
+  long long slots = two ? half : fit(kFewAllSmem);
+  if (early) slots = std::min<long long>(slots, 4);
+  if (slots < std::min<long long>(2, per_warp)) return false;
+  if (rounds > 1) {
+    const long long tiles = ((glu ? 2 * N : N) + 127) / 128;
+    if (tiles <= sms ? !two && !(early && T <= 2) : !glu && T > 8) return false;
+  }
   f->n_slots = static_cast<int>(slots);
   const int mt = f->pad > 32 ? 4 : 2, nt = T > 8 ? 2 : 1;
   const long long sums = 512LL * kFewWarps * mt * nt;      // the warps' sums take the place of slots and tokens
-  f->smem = static_cast<size_t>(1024 + kFewHead + std::max(slots * round + x, sums));
+  f->smem = static_cast<size_t>(1024 + kFewHead + std::max(slots * step + x, sums));
   return true;
 }
 
@@ -333,11 +362,11 @@ int launch_few(const FewPlan& f, const DenseProduct& d, bool early, uint32_t* am
 }
 
 // A product of K-major operands: few tokens take the streaming kernel (int8,
-// [4096, 7168]: 6.2 us at one token, 7.1 at 16; the split kernel 7.4 and 7.7).
+// [4096, 7168]: 5.3 us at one token, 7.0 at 16; the split kernel 7.4 and 7.8).
 template <int EPI>
 int launch_product(const DenseProduct& d, bool early, cudaStream_t s) {
   FewPlan f;
-  if (plan_few(&f, d.M, d.N, d.K * (epi_i8(EPI) ? 1 : 2), epi_glu(EPI)))
+  if (plan_few(&f, d.M, d.N, d.K * (epi_i8(EPI) ? 1 : 2), epi_glu(EPI), early))
     return launch_few<EPI, false>(f, d, early, nullptr, s);
   return launch_tiles<EPI, false, false>(d, early, s);
 }
@@ -496,7 +525,7 @@ extern "C" int stq1_i8_ffn(const uint16_t* x, const int8_t* gateup_q, const floa
   const DenseProduct up = i8_product(xq, sx, gateup_q, gateup_scales, act, T, N / 2, H);
   const DenseProduct down = i8_product(aq, sa, down_q, down_scales, out, T, H, N / 2);
   FewPlan fg, fd;
-  if (plan_few(&fg, T, N / 2, H, true) && plan_few(&fd, T, H, N / 2, false)) {
+  if (plan_few(&fg, T, N / 2, H, true, true) && plan_few(&fd, T, H, N / 2, false, true)) {
     // few tokens: each kernel asks for its weights while the one before it
     // still runs; the activation's maxima are kept by the kernel that writes
     // it, so that its codes are made inside the second product

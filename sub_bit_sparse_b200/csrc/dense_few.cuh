@@ -10,10 +10,11 @@
 // 13 us against 6 on [4096, 7168] int8.)
 //
 // Bound by HBM and by what a launch cannot avoid, about 3 us from its start to
-// the first bytes and from the last bytes to the stored sums: bf16 gated
-// [4096, 7168] at one token 12.0 us, 4.9 TB/s (58.7 MB alone would take 8.9);
-// int8 6.2 us at one token, 7.1 at 16.  (Loads straight into registers instead of
-// copies through shared memory: 7.7 and 14.3 us at one token.)
+// the first bytes and from the last bytes to the stored sums, of which a second
+// CTA on the SM hides a part: int8 [4096, 7168] at one token 5.3 us, 5.5 TB/s
+// (29.4 MB alone would take 4.5), 7.0 at 16; bf16 gated 12.2 us, 4.8 TB/s.  (Loads
+// straight into registers instead of copies through shared memory: 7.7 and 14.3
+// us at one token.)
 //
 // A contraction may take its k in any order as long as both operands agree on
 // it.  So a lane's share of an A fragment need not be the 4-byte pieces that
