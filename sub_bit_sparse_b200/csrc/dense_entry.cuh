@@ -19,8 +19,9 @@ bool dense_shape_ok(long long a, long long b, long long c) {
 }
 
 // 2-D map over a row-major matrix [rows, cols] whose boxes are 128 bytes of a
-// row by box_rows rows, in the 128-byte swizzle; what lies outside reads as zero.
-bool make_operand_map(CUtensorMap* map, const void* base, bool i8, long long rows, long long cols, int box_rows) {
+// row by box_rows rows, in the 128-byte swizzle or plain; what lies outside reads as zero.
+bool make_operand_map(CUtensorMap* map, const void* base, bool i8, long long rows, long long cols, int box_rows,
+                      bool swizzle = true) {
   auto fn = encode_fn();
   if (!fn) return false;
   const int es = i8 ? 1 : 2;
@@ -29,8 +30,9 @@ bool make_operand_map(CUtensorMap* map, const void* base, bool i8, long long row
   cuuint32_t box[2] = {static_cast<cuuint32_t>(kDnStepBytes / es), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t es1[2] = {1, 1};
   return fn(map, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), gdim,
-            gstride, box, es1, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            gstride, box, es1, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // 2-D map over results [rows, cols] (row stride ld elements) for copies of
@@ -302,16 +304,18 @@ struct FewPlan {
 // - more tiles than that: int8 above 8 tokens on tiles ([65536, 2048], 12 tokens:
 //   42.8 and 36.2 us; 8 tokens: 36.4 and 37.5), the gated form here ([28672, 4096],
 //   12 tokens: 52.0 and 63.0).
-bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu, bool early) {
+bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu, bool early, bool made = false) {
   if (T > kFewMaxTokens) return false;
   const int sms = sm_count(), unit = glu ? 8 : 16;         // the gate rows end on a whole swizzle atom
   const long long round_rows = sms * (glu ? 32LL : 64LL), rounds = (N + round_rows - 1) / round_rows;
   f->rows = static_cast<int>((N + sms * rounds - 1) / (sms * rounds));
   f->pad = (f->rows + unit - 1) / unit * unit * (glu ? 2 : 1);
   f->n_k = static_cast<int>((kbytes + kDnStepBytes - 1) / kDnStepBytes);
-  const long long x = few_pitch(f->n_k) * T;
+  const int mt = f->pad > 32 ? 4 : 2, nt = T > 8 ? 2 : 1;
+  const long long x = made ? few_pitch(f->n_k) * T : 0;
   const long long per_warp = (f->n_k + kFewWarps - 1) / kFewWarps;
-  const long long step = static_cast<long long>(f->pad) * kDnStepBytes * kFewWarps;      // one slot per warp
+  // one slot per warp, with its tokens
+  const long long step = (static_cast<long long>(f->pad) * kDnStepBytes + few_x_bytes(static_cast<int>(T), made)) * kFewWarps;
   auto fit = [&](long long smem) {
     return std::min<long long>(std::min<long long>((smem - 1024 - kFewHead - x) / step, per_warp), kFewMaxSlots);
   };
@@ -325,7 +329,6 @@ bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu, 
     if (tiles <= sms ? !two && !(early && T <= 2) : !glu && T > 8) return false;
   }
   f->n_slots = static_cast<int>(slots);
-  const int mt = f->pad > 32 ? 4 : 2, nt = T > 8 ? 2 : 1;
   const long long sums = 512LL * kFewWarps * mt * nt;      // the warps' sums take the place of slots and tokens
   f->smem = static_cast<size_t>(1024 + kFewHead + std::max(slots * step + x, sums));
   return true;
@@ -352,10 +355,12 @@ int launch_few(const FewPlan& f, const DenseProduct& d, bool early, uint32_t* am
   p.n_slots = f.n_slots;
   p.early = early;
   p.amax = amax;
-  CUtensorMap mw;
-  if (!make_operand_map(&mw, d.b, I8, GLU ? 2 * d.N : d.N, d.K, f.rows)) return STQ1_ERR_CUDA;
+  CUtensorMap mw, mx{};
+  if (!make_operand_map(&mw, d.b, I8, GLU ? 2 * d.N : d.N, d.K, f.rows) ||
+      (!MADE && !make_operand_map(&mx, d.a, I8, d.M, d.K, static_cast<int>(d.M), d.M > 1)))
+    return STQ1_ERR_CUDA;
   const unsigned grid = static_cast<unsigned>((d.N + f.rows - 1) / f.rows);
-  auto launch = [&](auto kernel) { return launch_pdl(kernel, grid, kFewThreads, f.smem, s, mw, p); };
+  auto launch = [&](auto kernel) { return launch_pdl(kernel, grid, kFewThreads, f.smem, s, mw, mx, p); };
   if (f.pad > 32)
     return d.M > 8 ? launch(dense_few_kernel<EPI, MADE, 4, 2>) : launch(dense_few_kernel<EPI, MADE, 4, 1>);
   return d.M > 8 ? launch(dense_few_kernel<EPI, MADE, 2, 2>) : launch(dense_few_kernel<EPI, MADE, 2, 1>);
@@ -525,7 +530,7 @@ extern "C" int stq1_i8_ffn(const uint16_t* x, const int8_t* gateup_q, const floa
   const DenseProduct up = i8_product(xq, sx, gateup_q, gateup_scales, act, T, N / 2, H);
   const DenseProduct down = i8_product(aq, sa, down_q, down_scales, out, T, H, N / 2);
   FewPlan fg, fd;
-  if (plan_few(&fg, T, N / 2, H, true, true) && plan_few(&fd, T, H, N / 2, false, true)) {
+  if (plan_few(&fg, T, N / 2, H, true, true) && plan_few(&fd, T, H, N / 2, false, true, true)) {
     // few tokens: each kernel asks for its weights while the one before it
     // still runs; the activation's maxima are kept by the kernel that writes
     // it, so that its codes are made inside the second product

@@ -11,10 +11,11 @@
 //
 // Bound by HBM and by what a launch cannot avoid, about 3 us from its start to
 // the first bytes and from the last bytes to the stored sums, of which a second
-// CTA on the SM hides a part: int8 [4096, 7168] at one token 5.3 us, 5.5 TB/s
-// (29.4 MB alone would take 4.5), 7.0 at 16; bf16 gated 12.2 us, 4.8 TB/s.  (Loads
-// straight into registers instead of copies through shared memory: 7.7 and 14.3
-// us at one token.)
+// CTA on the SM hides a part: int8 [4096, 7168] at one token 5.2 us, 5.6 TB/s
+// (29.4 MB alone would take 4.5), 6.6 at 16; bf16 gated 11.1 us, 5.3 TB/s, 12.6 at
+// 16.  (Loads straight into registers instead of copies through shared memory: 7.7
+// and 14.3 us at one token.)  The tokens' steps come beside the weights' as copies
+// of their own: brought whole before the first step, 16 tokens took 7.2 and 14.1.
 //
 // A contraction may take its k in any order as long as both operands agree on
 // it.  So a lane's share of an A fragment need not be the 4-byte pieces that
@@ -40,6 +41,7 @@ constexpr int kFewWarps = 8;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewMaxSlots = 8;              // steps in flight per warp
 constexpr int kFewHead = 1024;               // barriers and small arrays
+static_assert(8 * kFewMaxSlots * kFewWarps + 3 * 4 * kFewMaxTokens <= kFewHead, "");
 
 struct FewArgs {
   const void* x;               // [T, K] codes or bf16
@@ -57,7 +59,13 @@ struct FewArgs {
                                // output, raised (8-bit gated form), or NULL
 };
 
-// Bytes between tokens in shared memory: whole steps and 16 more, so that two
+// Bytes of a step of the tokens beside a slot: a lone token takes one plain row
+// (all lanes read it), more take groups of eight rows in the copies' swizzle; none
+// where their codes are made here.
+__host__ __device__ constexpr int few_x_bytes(int T, bool made) {
+  return made ? 0 : (T == 1 ? kDnStepBytes : (T + 7) / 8 * 8 * kDnStepBytes);
+}
+// Bytes between tokens whose codes are made here: whole steps and 16 more, so that two
 // tokens' pieces (every second one of a step) fall on different banks.
 __host__ __device__ constexpr long long few_pitch(int n_k) { return n_k * 128LL + 16; }
 
@@ -82,7 +90,7 @@ __device__ __forceinline__ void few_mma(float (&c)[4], uint32_t a0, uint32_t a1,
 // MT: fragments of 16 weight rows (at most); NT: groups of 8 tokens.
 template <int EPI, bool MADE, int MT, int NT>
 __global__ void __launch_bounds__(kFewThreads, 2)
-dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
+dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const FewArgs p) {
   constexpr bool I8 = epi_i8(EPI), GLU = epi_glu(EPI);
   static_assert(I8 || !MADE, "codes are made for 8-bit weights");
   using Acc = std::conditional_t<I8, int, float>;
@@ -92,28 +100,34 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
   const uint32_t sraw = smem_u32(smem_raw);
   const uint32_t sbase = (sraw + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t s_scale = sbase + 8 * kFewMaxSlots * kFewWarps, bar_x = s_scale + 64;
-  const uint32_t slot_bytes = p.pad * kDnStepBytes;
+  // the warps' barriers, then 16 words each of scales, their inverses and largest outputs
+  const uint32_t s_scale = sbase + 8 * kFewMaxSlots * kFewWarps, s_inv_at = s_scale + 64, s_amax_at = s_inv_at + 64;
+  const uint32_t slot_bytes = p.pad * kDnStepBytes, x_bytes = few_x_bytes(p.T, MADE);
   const uint32_t s_w = sbase + kFewHead;                               // the warps' slots
-  const uint32_t s_x = s_w + kFewWarps * p.n_slots * slot_bytes;       // the tokens
+  const uint32_t s_x = s_w + kFewWarps * p.n_slots * slot_bytes;       // the slots' tokens, or (MADE) their codes
   const uint32_t pitch = static_cast<uint32_t>(few_pitch(p.n_k));
   const uint32_t my_bar = sbase + 8 * kFewMaxSlots * warp;
-  const uint32_t my_slots = s_w + warp * p.n_slots * slot_bytes;
+  const uint32_t my_slots = s_w + warp * p.n_slots * slot_bytes, my_x = s_x + warp * p.n_slots * x_bytes;
   const long long n0 = static_cast<long long>(blockIdx.x) * p.rows;
 
   // ---- this warp's first steps ----
   const int y0 = static_cast<int>(n0), y1 = static_cast<int>(p.N + n0);
-  const uint32_t step_bytes = (GLU ? 2 : 1) * p.rows * kDnStepBytes;
+  const uint32_t step_bytes = ((GLU ? 2 : 1) * p.rows + (MADE ? 0 : p.T)) * kDnStepBytes;
   auto fetch = [&](int step, int slot) {                               // lane 0 only
     const uint32_t bar = my_bar + 8 * slot, dst = my_slots + slot * slot_bytes;
     mbar_arrive_expect_tx(bar, step_bytes);
     dn_load<1>(dst, &map_w, step * kStep, y0, bar);
     if constexpr (GLU) dn_load<1>(dst + slot_bytes / 2, &map_w, step * kStep, y1, bar);
   };
-  if (threadIdx.x == 0) dn_prefetch_map(&map_w);
+  auto fetch_x = [&](int step, int slot) {                             // and its tokens
+    if constexpr (!MADE) dn_load<1>(my_x + slot * x_bytes, &map_x, step * kStep, 0, my_bar + 8 * slot);
+  };
+  if (threadIdx.x == 0) {
+    dn_prefetch_map(&map_w);
+    if constexpr (!MADE) dn_prefetch_map(&map_x);
+  }
   if (lane == 0) {
     for (int i = 0; i < p.n_slots; ++i) mbar_init(my_bar + 8 * i, 1);
-    if (warp == 0) mbar_init(bar_x, 1);
     fence_mbar_init();
   }
   __syncwarp();
@@ -125,50 +139,55 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
     for (int i = 0; i < p.n_slots && warp + kFewWarps * i < p.n_k; ++i) fetch(warp + kFewWarps * i, i);
   if (p.early) griddep_wait();
   griddep_launch_dependents();
+  if (lane == 0)
+    for (int i = 0; i < p.n_slots && warp + kFewWarps * i < p.n_k; ++i) fetch_x(warp + kFewWarps * i, i);
 
-  // ---- the tokens into shared memory ----
-  const long long kbytes = p.K * ES;
   if constexpr (MADE) {
-    // the warps share out the tokens: one warp each, or with fewer tokens 2, 4 or 8
-    const int per = p.T > 4 ? 1 : (p.T > 2 ? 2 : (p.T > 1 ? 4 : 8));
-    const int nv = static_cast<int>(p.K / 16);
-    for (int tok = warp / per; tok < p.T; tok += kFewWarps / per) {
-      const char* xr = static_cast<const char*>(p.x) + tok * p.K * 2;
-      const I8Scale sc = i8_scale(__ldcg(p.amax + tok));
-      const int first = (warp % per) * 32 + lane;
-      if (first == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_scale + 4 * tok), "f"(sc.scale) : "memory");
-#pragma unroll 4
-      for (int i = first; i < nv; i += 32 * per) {
-        Row8<false> a, b;
-        a.load(xr, 2 * i);
-        b.load(xr, 2 * i + 1);
-        const uint2 lo = a.codes(sc.inv), hi = b.codes(sc.inv);
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(s_x + tok * pitch + 16 * i), "r"(lo.x), "r"(lo.y),
-                     "r"(hi.x), "r"(hi.y)
-                     : "memory");
+    // 16 values a piece, the CTA's pieces dealt out to all threads, eight loads
+    // of each thread in flight (a warp per token took 1 us more at 16 tokens)
+    constexpr int kMany = 4;
+    const int nv = static_cast<int>(p.K / 16), total = nv * p.T;
+    float* s_inv = reinterpret_cast<float*>(smem_raw + (s_inv_at - sraw));
+    if (threadIdx.x < p.T) {
+      const I8Scale sc = i8_scale(__ldcg(p.amax + threadIdx.x));
+      s_inv[threadIdx.x] = sc.inv;
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_scale + 4 * threadIdx.x), "f"(sc.scale) : "memory");
+    }
+    for (int i0 = threadIdx.x; i0 < total + static_cast<int>(threadIdx.x); i0 += kMany * kFewThreads) {
+      Row8<false> a[kMany], b[kMany];
+#pragma unroll
+      for (int j = 0; j < kMany; ++j) {
+        const int i = i0 + j * kFewThreads;
+        if (i < total) {                             // (the tokens' rows lie one after another)
+          a[j].load(p.x, 2 * i);
+          b[j].load(p.x, 2 * i + 1);
+        }
+      }
+      if (i0 == static_cast<int>(threadIdx.x)) __syncthreads();   // the scales
+#pragma unroll
+      for (int j = 0; j < kMany; ++j) {
+        const int i = i0 + j * kFewThreads;
+        if (i < total) {
+          const int tok = i / nv;
+          const float inv = s_inv[tok];
+          const uint2 lo = a[j].codes(inv), hi = b[j].codes(inv);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(s_x + tok * pitch + 16 * (i - tok * nv)), "r"(lo.x),
+                       "r"(lo.y), "r"(hi.x), "r"(hi.y)
+                       : "memory");
+        }
       }
     }
-  } else {
-    // one bulk copy per token (K * ES and the pitch are multiples of 16 bytes)
-    if (threadIdx.x == 0) {
-      mbar_arrive_expect_tx(bar_x, static_cast<uint32_t>(p.T * kbytes));
-      for (int tok = 0; tok < p.T; ++tok)
-        bulk_g2s(s_x + tok * pitch, static_cast<const char*>(p.x) + tok * kbytes, static_cast<uint32_t>(kbytes), bar_x);
-    }
-  }
-  {
-    // K past its end within the last step: the weights read as zero there, and so must the tokens (0 * NaN)
-    const int end = static_cast<int>(kbytes / 16), tail = p.n_k * 8 - end;
+    // K past its end within the last step: the weights read as zero there, and so must the tokens
+    const int tail = p.n_k * 8 - nv;
     for (int i = threadIdx.x; i < tail * p.T; i += kFewThreads)
-      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(s_x + (i / tail) * pitch + 16 * (end + i % tail)), "r"(0u)
+      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(s_x + (i / tail) * pitch + 16 * (nv + i % tail)), "r"(0u)
                    : "memory");
+    __syncthreads();
   }
-  __syncthreads();
-  bool ok = MADE || mbar_wait_bounded(bar_x, 0);
+  bool ok = true;
 
   // ---- this warp's steps ----
   const int mt = p.pad >> 4;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
   Acc acc[MT][NT][4] = {};
   // rows of a fragment in a slot, and this lane's pieces of them
   const uint32_t up = GLU ? slot_bytes / 2 : 8 * kDnStepBytes;         // from row g to the row of fragment row g + 8
@@ -176,20 +195,26 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
   const uint32_t off0 = g * kDnStepBytes + (((2 * t) ^ g) << 4), off1 = g * kDnStepBytes + (((2 * t + 1) ^ g) << 4);
   int slot = 0;
   uint32_t ph = 0;
-  for (int step = warp; ok && step < p.n_k; step += kFewWarps) {
+  for (int step = warp; step < p.n_k; step += kFewWarps) {
     if (!mbar_wait_bounded(my_bar + 8 * slot, ph)) {
       ok = false;
       break;                                         // (its own copies have had that wait to land)
     }
-    uint4 x0[NT], x1[NT];
+    const uint32_t base = my_slots + slot * slot_bytes;
+    uint4 x0[NT], x1[NT];                            // (what stands for a token past the last is not stored)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const bool token = 8 * n + g < p.T;
-      const uint32_t at = s_x + (8 * n + g) * pitch + step * kDnStepBytes + 32 * t;
-      x0[n] = token ? lds_v4(at) : zero;
-      x1[n] = token ? lds_v4(at + 16) : zero;
+      if constexpr (MADE) {
+        const bool token = 8 * n + g < p.T;
+        const uint32_t at = s_x + (8 * n + g) * pitch + step * kDnStepBytes + 32 * t;
+        x0[n] = token ? lds_v4(at) : make_uint4(0, 0, 0, 0);
+        x1[n] = token ? lds_v4(at + 16) : make_uint4(0, 0, 0, 0);
+      } else {
+        const uint32_t at = my_x + slot * x_bytes + n * 8 * kDnStepBytes;
+        x0[n] = lds_v4(at + (p.T == 1 ? 32 * t : off0));
+        x1[n] = lds_v4(at + (p.T == 1 ? 32 * t + 16 : off1));
+      }
     }
-    const uint32_t base = my_slots + slot * slot_bytes;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       if (i < mt) {
@@ -207,7 +232,10 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
     }
     __syncwarp();                                    // every lane has read the slot
     const int next = step + kFewWarps * p.n_slots;
-    if (lane == 0 && next < p.n_k) fetch(next, slot);
+    if (lane == 0 && next < p.n_k) {
+      fetch(next, slot);
+      fetch_x(next, slot);
+    }
     if (++slot == p.n_slots) slot = 0, ph ^= 1;
   }
   __syncthreads();                                   // the slots are free: the warps' sums take their place
@@ -221,7 +249,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const FewArgs p) {
                    "r"(*reinterpret_cast<const uint32_t*>(&acc[i][n][2])), "r"(*reinterpret_cast<const uint32_t*>(&acc[i][n][3]))
                    : "memory");
   // the CTA's largest outputs of each token (8-bit gated form)
-  uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem_raw + (bar_x + 8 - sraw));
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem_raw + (s_amax_at - sraw));
   if (EPI == kEpiI8Glu && threadIdx.x < kFewMaxTokens) s_amax[threadIdx.x] = 0u;
   if (__syncthreads_or(!ok)) return;                 // a wait ran out (flagged): nothing is stored
 
