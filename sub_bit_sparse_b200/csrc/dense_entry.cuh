@@ -287,24 +287,21 @@ struct FewPlan {
   int rows, pad, n_k, n_slots;
   size_t smem;
 };
-// false: the tile kernels take it.  early: the weights are asked for before the
-// kernel before has run.  The rules, each with both sides measured:
+// false: the tile kernels take it.  made: the kernel makes the tokens' codes.
+// The rules, each with both sides measured:
 // - a CTA whose weights are read quickly (up to 256 KB) leaves room for a second
 //   one on its SM, so that the next launch starts beside it: int8 [4096, 7168] at
 //   one token 5.9 -> 5.3 us, gated [2048, 7168] 8.7 -> 7.7; with 400 KB, gated
-//   [4096, 7168], the steps in flight count for more: 12.2 and 12.7.
-// - early, no more than four steps per warp: a deeper queue of copies holds up
-//   the tokens' codes (8-bit layer of [4096, 7168], 8 tokens 16.5 -> 15.8 us).
+//   [4096, 7168], the steps in flight count for more: 11.2 and 11.7.
 // - more outputs than one round of CTAs, and single tiles that run at once: the
-//   tiles (int8 [16384, 4096]: 15.7 us and 14.3 on tiles at one token, 20.1 and
-//   14.7 at 16), except where the rounds overlap because two CTAs fit an SM
-//   ([11008, 4096] at one token 9.8 and 11.9), and in the 8-bit layer up to two
-//   tokens, where it saves the launch for the codes (25.6 us against 27.8 for a
-//   layer of [16384, 4096]).
+//   tiles (int8 [16384, 4096]: 15.1 us and 14.3 on tiles at one token, 18.3 and
+//   14.6 at 16; gated [14336, 4096] at 12 tokens 26.9 and 24.8), except gated up
+//   to 8 tokens (22.3 and 24.7 at one) and where the rounds overlap because two
+//   CTAs fit an SM (int8 [11008, 4096] at one token 9.5 and 12.1).
 // - more tiles than that: int8 above 8 tokens on tiles ([65536, 2048], 12 tokens:
-//   42.8 and 36.2 us; 8 tokens: 36.4 and 37.5), the gated form here ([28672, 4096],
-//   12 tokens: 52.0 and 63.0).
-bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu, bool early, bool made = false) {
+//   40.1 and 36.3 us; 8 tokens: 34.6 and 36.2), the gated form here ([28672, 4096],
+//   12 tokens: 48.9 and 63.3).
+bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu, bool made = false) {
   if (T > kFewMaxTokens) return false;
   const int sms = sm_count(), unit = glu ? 8 : 16;         // the gate rows end on a whole swizzle atom
   const long long round_rows = sms * (glu ? 32LL : 64LL), rounds = (N + round_rows - 1) / round_rows;
@@ -321,12 +318,11 @@ bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu, 
   };
   const long long half = fit(kFewHalfSmem);
   const bool two = f->rows * (glu ? 2 : 1) * kbytes <= 256 * 1024 && half >= std::min<long long>(2, per_warp);
-  long long slots = two ? half : fit(kFewAllSmem);
-  if (early) slots = std::min<long long>(slots, 4);
+  const long long slots = two ? half : fit(kFewAllSmem);
   if (slots < std::min<long long>(2, per_warp)) return false;
   if (rounds > 1) {
     const long long tiles = ((glu ? 2 * N : N) + 127) / 128;
-    if (tiles <= sms ? !two && !(early && T <= 2) : !glu && T > 8) return false;
+    if (tiles <= sms ? !two && !(glu && T <= 8) : !glu && T > 8) return false;
   }
   f->n_slots = static_cast<int>(slots);
   const long long sums = 512LL * kFewWarps * mt * nt;      // the warps' sums take the place of slots and tokens
@@ -371,7 +367,7 @@ int launch_few(const FewPlan& f, const DenseProduct& d, bool early, uint32_t* am
 template <int EPI>
 int launch_product(const DenseProduct& d, bool early, cudaStream_t s) {
   FewPlan f;
-  if (plan_few(&f, d.M, d.N, d.K * (epi_i8(EPI) ? 1 : 2), epi_glu(EPI), early))
+  if (plan_few(&f, d.M, d.N, d.K * (epi_i8(EPI) ? 1 : 2), epi_glu(EPI)))
     return launch_few<EPI, false>(f, d, early, nullptr, s);
   return launch_tiles<EPI, false, false>(d, early, s);
 }
@@ -530,7 +526,7 @@ extern "C" int stq1_i8_ffn(const uint16_t* x, const int8_t* gateup_q, const floa
   const DenseProduct up = i8_product(xq, sx, gateup_q, gateup_scales, act, T, N / 2, H);
   const DenseProduct down = i8_product(aq, sa, down_q, down_scales, out, T, H, N / 2);
   FewPlan fg, fd;
-  if (plan_few(&fg, T, N / 2, H, true, true) && plan_few(&fd, T, H, N / 2, false, true, true)) {
+  if (plan_few(&fg, T, N / 2, H, true) && plan_few(&fd, T, H, N / 2, false, true)) {
     // few tokens: each kernel asks for its weights while the one before it
     // still runs; the activation's maxima are kept by the kernel that writes
     // it, so that its codes are made inside the second product
