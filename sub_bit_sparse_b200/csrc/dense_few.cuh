@@ -44,11 +44,11 @@ constexpr int kFewHead = 1024;               // barriers and small arrays
 static_assert(8 * kFewMaxSlots * kFewWarps + 3 * 4 * kFewMaxTokens <= kFewHead, "");
 
 struct FewArgs {
-  const void* x;               // [T, K] codes or bf16
+  const void* x;               // MADE: [T, K] bf16 (else by tensor copies)
   const float *sx, *sw;
   void* out;
   uint16_t* y;
-  long long N, K;              // outputs (for the gated forms half of the weight rows); values per row
+  long long N, K;              // outputs (for the gated forms half of the weight rows); values per row (MADE)
   int T;
   int rows;                    // outputs per CTA
   int pad;                     // weight rows of one step in shared memory (a multiple of 16)
@@ -85,8 +85,8 @@ __device__ __forceinline__ void few_mma(float (&c)[4], uint32_t a0, uint32_t a1,
 // MADE: x is bf16 and its codes are made here, from each token's largest
 // magnitude, which the kernel that wrote x kept (the down projection of the
 // 8-bit layer).  For the first projection the magnitudes would have to be found
-// by every CTA, which took longer than a launch of its own: 15.7 us against
-// 15.5 for the layer at one token, 18.9 against 16.4 at four.
+// by every CTA, which takes longer than a launch of its own (at four tokens of a
+// [4096, 7168] layer by 2.5 us).
 // MT: fragments of 16 weight rows (at most); NT: groups of 8 tokens.
 template <int EPI, bool MADE, int MT, int NT>
 __global__ void __launch_bounds__(kFewThreads, 2)
@@ -144,7 +144,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 
   if constexpr (MADE) {
     // 16 values a piece, the CTA's pieces dealt out to all threads, eight loads
-    // of each thread in flight (a warp per token took 1 us more at 16 tokens)
+    // of each thread in flight (a warp per token took 0.5 us more at 16 tokens)
     constexpr int kMany = 4;
     const int nv = static_cast<int>(p.K / 16), total = nv * p.T;
     float* s_inv = reinterpret_cast<float*>(smem_raw + (s_inv_at - sraw));

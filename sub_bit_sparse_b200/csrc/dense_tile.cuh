@@ -264,7 +264,8 @@ __device__ __forceinline__ void dn_store_copy(const uint32_t* w, uint32_t buf, c
 }
 // The same (blocks of 32 words a row) for rows that tensor copies cannot
 // address, because a row's bytes are no multiple of 16: a row at a time, a lane
-// per word.
+// per word (4096 tokens by [2053, 2048]: 21.1 us with fp32 results, 21.6 with
+// bf16; by copies, [2056, 2048], 20.9).
 template <int ES>
 __device__ __forceinline__ void dn_store_plain(const uint32_t* w, uint32_t buf, void* out, long long row0,
                                                long long rows, long long ld, long long col0, long long cols) {

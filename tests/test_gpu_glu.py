@@ -62,6 +62,8 @@ SHAPES = [
     (257, 528, 264), (300, 4096, 640), (513, 1040, 1032), (1000, 2048, 512), (1100, 528, 2056),
     (2600, 1072, 264), (2000, 2704, 72), (4000, 528, 136),
     (1600, 2064, 1544), (2100, 2112, 1160), (700, 4096, 3600),
+    # few tokens: outputs for more than one round of CTAs, one or two CTAs per SM, rows longer than what is in flight
+    (1, 9488, 72), (8, 9600, 40), (9, 9600, 40), (16, 19200, 24), (1, 20000, 16), (1, 64, 16392), (16, 160, 8200),
 ]
 
 

@@ -91,6 +91,9 @@ SHAPES = [  # T, N, K: every token count where a kernel changes, and its neighbo
     (128, 4096, 2048), (129, 130, 112), (200, 1000, 3600), (255, 512, 16), (256, 256, 512), (257, 259, 272),
     (300, 4096, 1024), (512, 777, 1296), (700, 2048, 512), (1000, 1025, 1040), (1500, 4096, 256), (2049, 513, 384),
     (2500, 1001, 272), (2500, 1004, 64), (2561, 2056, 16), (5000, 600, 144), (4100, 4098, 48), (20000, 130, 32),
+    # few tokens: outputs for more than one round of CTAs, one or two CTAs per SM, rows longer than what is in flight
+    (1, 11008, 144), (2, 9473, 272), (3, 9500, 2064), (8, 18960, 48), (9, 20001, 32), (16, 9473, 80), (12, 25000, 16),
+    (1, 200, 32784), (5, 70, 20000), (16, 70, 20000), (2, 20, 131056), (13, 5000, 1040),
 ]
 
 
@@ -143,7 +146,8 @@ def _layer(rng, n, h):
 @pytest.mark.parametrize("t,n,h", [(1, 32, 16), (1, 4096, 7168), (2, 96, 272), (3, 2080, 1040), (8, 512, 512),
                                    (9, 160, 128), (16, 1024, 1536), (17, 224, 208), (32, 256, 512), (33, 256, 512),
                                    (65, 544, 336), (128, 1024, 256), (130, 288, 1040), (300, 512, 512),
-                                   (520, 1056, 784), (1030, 512, 256)])
+                                   (520, 1056, 784), (1030, 512, 256), (1, 9600, 64), (2, 9632, 80), (8, 19200, 32),
+                                   (9, 9600, 48), (3, 64, 9600), (16, 96, 9600), (7, 32, 20016), (4, 16416, 32)])
 def test_layer_gives_the_bits_of_the_chain(t, n, h):
     rng = np.random.default_rng(t + n + h)
     x, xv = _bf16(rng.standard_normal((t, h)) * 2)
