@@ -290,9 +290,13 @@ struct FewPlan {
 // false: the tile kernels take it.  made: the kernel makes the tokens' codes.
 // The rules, each with both sides measured:
 // - a CTA whose weights are read quickly (up to 256 KB) leaves room for a second
-//   one on its SM, so that the next launch starts beside it: int8 [4096, 7168] at
-//   one token 5.9 -> 5.3 us, gated [2048, 7168] 8.7 -> 7.7; with 400 KB, gated
-//   [4096, 7168], the steps in flight count for more: 11.2 and 11.7.
+//   one on its SM, so that the next launch starts beside it (int8 [4096, 7168] at
+//   one token, weights partly in L2: 5.9 -> 5.2 us; gated [2048, 7168] 8.7 -> 7.7),
+//   unless too few steps were left in flight: with two of seven 16 tokens take 8.5
+//   us from HBM and with four 8.0.  Nor are there more than four, which queue up
+//   before HBM (int8 [2048, 7168] 5.9 us with six, 5.4 with four).
+// - with more bytes a CTA, gated [4096, 7168], the steps in flight count for more:
+//   10.9 us with six, 11.4 with three.
 // - more outputs than one round of CTAs, and single tiles that run at once: the
 //   tiles (int8 [16384, 4096]: 15.1 us and 14.3 on tiles at one token, 18.3 and
 //   14.6 at 16; gated [14336, 4096] at 12 tokens 26.9 and 24.8), except gated up
@@ -313,11 +317,13 @@ bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu, 
   const long long per_warp = (f->n_k + kFewWarps - 1) / kFewWarps;
   // one slot per warp, with its tokens
   const long long step = (static_cast<long long>(f->pad) * kDnStepBytes + few_x_bytes(static_cast<int>(T), made)) * kFewWarps;
+  const bool brief = f->rows * (glu ? 2 : 1) * kbytes <= 256 * 1024;
   auto fit = [&](long long smem) {
-    return std::min<long long>(std::min<long long>((smem - 1024 - kFewHead - x) / step, per_warp), kFewMaxSlots);
+    return std::min<long long>(std::min<long long>((smem - 1024 - kFewHead - x) / step, per_warp),
+                               brief ? 4 : kFewMaxSlots);
   };
   const long long half = fit(kFewHalfSmem);
-  const bool two = f->rows * (glu ? 2 : 1) * kbytes <= 256 * 1024 && half >= std::min<long long>(2, per_warp);
+  const bool two = brief && half >= std::min(per_warp, std::max(2LL, std::min(3LL, (per_warp + 1) / 2)));
   const long long slots = two ? half : fit(kFewAllSmem);
   if (slots < std::min<long long>(2, per_warp)) return false;
   if (rounds > 1) {
