@@ -2,7 +2,7 @@
 // CPython extension over PyTorch's C++ tensors: the checks, the outputs that
 // the caller does not give, the current stream, one call of the C ABI.
 //
-// These calls are short (6 us of device time for one token), and the same
+// These calls are short (5 to 7 us of device time for one token), and the same
 // steps made from Python, attribute by attribute, took 6 us of host time a
 // call besides the launch itself.  The extension holds no computation and does
 // not link the library: the package hands it the entry points' addresses, so

@@ -207,7 +207,7 @@ __device__ __forceinline__ void dn_tile_pos(const DenseArgs& p, int tile, int& t
 //               two gradients of 4096 tokens by [4096, 7168])
 //   warp 9      MMAs of the pair (leader)
 // Bound by the tensor pipe and, in a sustained loop, by the power limit: int8
-// 4096 tokens by [4096, 7168] 80-82 us cold (2.95 PFLOP/s), 95 sustained at
+// 4096 tokens by [4096, 7168] 78-82 us cold (3.0 PFLOP/s), 95 sustained at
 // lower clocks, 70 with all codes zero; tensor pipe 76% of the active cycles,
 // the rest start, last epilogue and an uneven last round.
 // ---------------------------------------------------------------------------
@@ -265,7 +265,7 @@ __device__ __forceinline__ void dn_store_copy(const uint32_t* w, uint32_t buf, c
 // The same (blocks of 32 words a row) for rows that tensor copies cannot
 // address, because a row's bytes are no multiple of 16: a row at a time, a lane
 // per word (4096 tokens by [2053, 2048]: 21.1 us with fp32 results, 21.6 with
-// bf16; by copies, [2056, 2048], 20.9).
+// bf16; by copies, [2056, 2048], 18.6 and 17.2).
 template <int ES>
 __device__ __forceinline__ void dn_store_plain(const uint32_t* w, uint32_t buf, void* out, long long row0,
                                                long long rows, long long ld, long long col0, long long cols) {
@@ -626,7 +626,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 // Products with few tiles: one CTA per 128 x 128 tile and piece of K.  Bound by
 // the copies into shared memory: 32 KB per step in 436 cycles (75 bytes a clock)
 // where the MMAs take 256; below about 128 tokens by the weights' way from HBM.
-// [4096, 7168] int8: 8.9 us at 64 tokens, 10.2 at 128, 13.1 at 256, 19.1 at 512.
+// [4096, 7168] int8: 9.1 us at 64 tokens, 10.6 at 128, 13.4 at 256, 18.0 at 512.
 // (Prefetching the weights into L2 as well, from idle warps, is 5-18% slower.)
 // ---------------------------------------------------------------------------
 
