@@ -54,7 +54,7 @@ bool make_result_map(CUtensorMap* map, void* base, bool f32, long long rows, lon
 
 std::atomic<bool> g_dense_configured[kMaxDevices];
 constexpr int kFewAllSmem = 232448;        // of one CTA on an SM
-constexpr int kFewHalfSmem = 233472 / 2 - 1024;   // of each of two (an SM has 228 KB and keeps 1 KB per CTA)
+constexpr int kFewHalfSmem = 233472 / 2 - 1024;   // two CTAs of so much fit (an SM has 228 KB and keeps 1 KB per CTA)
 template <int EPI, bool MADE, int MT, int NT>
 bool few_config_one() {
   return cudaFuncSetAttribute(dense_few_kernel<EPI, MADE, MT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -289,14 +289,13 @@ struct FewPlan {
 };
 // false: the tile kernels take it.  made: the kernel makes the tokens' codes.
 // The rules, each with both sides measured:
-// - a CTA whose weights are read quickly (up to 256 KB) leaves room for a second
-//   one on its SM, so that the next launch starts beside it (int8 [4096, 7168] at
-//   one token, weights partly in L2: 5.9 -> 5.2 us; gated [2048, 7168] 8.7 -> 7.7),
-//   unless too few steps were left in flight: with two of seven 16 tokens take 8.5
-//   us from HBM and with four 8.0.  Nor are there more than four, which queue up
-//   before HBM (int8 [2048, 7168] 5.9 us with six, 5.4 with four).
-// - with more bytes a CTA, gated [4096, 7168], the steps in flight count for more:
-//   10.9 us with six, 11.4 with three.
+// - a CTA whose weights are read quickly (up to 256 KB) has at most four steps in
+//   flight per warp, more queue up before HBM (int8 [2048, 7168] at one token 5.9
+//   us with six, 5.4 with four); with more bytes, gated [4096, 7168], they count
+//   for more: 10.9 us with six, 11.4 with three.
+// - one CTA per SM, but for the shortest: two hide a part of the next launch (int8
+//   [4096, 7168] 5.7 -> 5.0 us), until two of the same launch come to share an SM
+//   and others stand idle, which then stays so from call to call: 12 us.
 // - more outputs than one round of CTAs, and single tiles that run at once: the
 //   tiles (int8 [16384, 4096]: 15.1 us and 14.3 on tiles at one token, 18.3 and
 //   14.6 at 16; gated [14336, 4096] at 12 tokens 26.9 and 24.8), except gated up
@@ -317,22 +316,18 @@ bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu, 
   const long long per_warp = (f->n_k + kFewWarps - 1) / kFewWarps;
   // one slot per warp, with its tokens
   const long long step = (static_cast<long long>(f->pad) * kDnStepBytes + few_x_bytes(static_cast<int>(T), made)) * kFewWarps;
-  const bool brief = f->rows * (glu ? 2 : 1) * kbytes <= 256 * 1024;
-  auto fit = [&](long long smem) {
-    return std::min<long long>(std::min<long long>((smem - 1024 - kFewHead - x) / step, per_warp),
-                               brief ? 4 : kFewMaxSlots);
-  };
-  const long long half = fit(kFewHalfSmem);
-  const bool two = brief && half >= std::min(per_warp, std::max(2LL, std::min(3LL, (per_warp + 1) / 2)));
-  const long long slots = two ? half : fit(kFewAllSmem);
+  const long long bytes = f->rows * (glu ? 2 : 1) * kbytes;
+  const long long slots = std::min<long long>(std::min<long long>((kFewAllSmem - 1024 - kFewHead - x) / step, per_warp),
+                                              bytes <= 256 * 1024 ? 4 : kFewMaxSlots);
   if (slots < std::min<long long>(2, per_warp)) return false;
   if (rounds > 1) {
     const long long tiles = ((glu ? 2 * N : N) + 127) / 128;
-    if (tiles <= sms ? !two && !(glu && T <= 8) : !glu && T > 8) return false;
+    if (tiles <= sms ? !(glu && T <= 8) : !glu && T > 8) return false;
   }
   f->n_slots = static_cast<int>(slots);
   const long long sums = 512LL * kFewWarps * mt * nt;      // the warps' sums take the place of slots and tokens
   f->smem = static_cast<size_t>(1024 + kFewHead + std::max(slots * step + x, sums));
+  if (bytes > 64 * 1024) f->smem = std::max(f->smem, static_cast<size_t>(kFewHalfSmem + 16));
   return true;
 }
 
@@ -369,7 +364,7 @@ int launch_few(const FewPlan& f, const DenseProduct& d, bool early, uint32_t* am
 }
 
 // A product of K-major operands: few tokens take the streaming kernel (int8,
-// [4096, 7168]: 5.0 us at one token, 6.8 at 16; the split kernel 7.4 and 7.8).
+// [4096, 7168]: 5.2 us at one token, 6.8 at 16; the split kernel 7.4 and 7.8).
 template <int EPI>
 int launch_product(const DenseProduct& d, bool early, cudaStream_t s) {
   FewPlan f;
