@@ -71,7 +71,12 @@ __device__ __forceinline__ float i8_value(int acc, float sx, float sw) {
 //    reciprocal by one Newton step from fp32's.  Short, because a warp comes
 //    here about once per tile: with exp, a division and a general rounding the
 //    instruction fetches alone took the 4096-token int8 layer from 163 to 196 us.
-// 3. Values near the ends of fp32's range and NaN as swiglu_kernel does.
+//    It builds 2^k in the exponent's bits and so takes gates below 700 only
+//    (k > -1011; from below, |SiLU(g)| > 1e-30 keeps g above -74), and leaves to
+//    step 3 what lies within 2^-40 of the midpoint, exact midpoints among it: its
+//    own error then decides nothing.
+// 3. Those, farther gates, values near the ends of fp32's range and NaN as
+//    swiglu_kernel does.
 __device__ __noinline__ uint32_t swiglu_bf16_ends(float g, float u) {
   const double gd = g;
   return bf16_bits_from_f64(gd / (1.0 + exp(-gd)) * static_cast<double>(u));
@@ -92,9 +97,11 @@ __device__ __noinline__ uint32_t swiglu_bf16_border(float g, float u) {
   double rc = static_cast<double>(__frcp_rn(static_cast<float>(d)));
   rc = fma(rc, fma(-d, rc, 1.0), rc);
   const double v = static_cast<double>(g) * static_cast<double>(u) * rc;
-  // 19 bits: sign, 11 of exponent, 7 of mantissa, rounded to nearest, ties to even
+  // 19 bits: sign, 11 of exponent, 7 of mantissa, rounded to nearest; 2^12 of the
+  // 52 mantissa bits' units are 2^-40
   const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v));
-  const uint32_t q = static_cast<uint32_t>((b + ((1ull << 44) - 1) + ((b >> 45) & 1)) >> 45);
+  if ((b & ((1ull << 45) - 1)) - ((1ull << 44) - (1ull << 12)) <= 1ull << 13) return swiglu_bf16_ends(g, u);
+  const uint32_t q = static_cast<uint32_t>((b + (1ull << 44)) >> 45);
   return ((q & 0x3FFFFu) - (896u << 7)) | ((q >> 18) << 15);
 }
 // The fp32 step: bits rounded from v; false where another step must decide.
@@ -107,9 +114,10 @@ __device__ __forceinline__ bool swiglu_bf16_fast(float g, float u, uint32_t& bit
 }
 __device__ __noinline__ uint32_t swiglu_bf16_slow(float g, float u) {
   const float s = __fdividef(g, 1.f + expf(-g)), v = s * u;
-  // a zero gate or up, as a padded batch has whole rows of (0 * Inf is NaN and goes on)
-  if (v == 0.f && (g == 0.f || u == 0.f)) return __float_as_uint(v) >> 16;
-  if (fabsf(s) > 1e-30f && fabsf(v) > 1e-30f && fabsf(v) < 1e38f) return swiglu_bf16_border(g, u);
+  // a zero gate or up, as a padded batch has whole rows of (0 * Inf is NaN and goes on);
+  // its sign is that of the factors, as s may itself have been flushed to a zero of any sign
+  if (v == 0.f && (g == 0.f || u == 0.f)) return ((__float_as_uint(g) ^ __float_as_uint(u)) >> 31) << 15;
+  if (fabsf(s) > 1e-30f && fabsf(v) > 1e-30f && fabsf(v) < 1e38f && g < 700.f) return swiglu_bf16_border(g, u);
   return swiglu_bf16_ends(g, u);
 }
 __device__ __forceinline__ uint32_t swiglu_bf16(float g, float u) {
