@@ -439,6 +439,20 @@ int stq1_set_path(int path);
 int stq1_selftest_wait(int arrive, void* stream);
 
 /*
+ * stq1_selftest_product -- the same for the waits of the tensor-core tile
+ * kernels: stq1_i8_matmul with fp32 results, on those kernels for any T.  With
+ * arrive = 0 each step of K waits for 16 bytes more than its copies bring, so
+ * that the wait for the first step gives up: STQ1_DEV_WAIT_LIMIT is recorded,
+ * y is left as it was, and the kernel returns within four seconds; the context
+ * stays usable.  With arrive = 1 it is the plain product.  Arguments as for
+ * stq1_i8_matmul.  Asynchronous on `stream`.
+ * Errors: STQ1_ERR_NULL, STQ1_ERR_ARG (arrive not 0 or 1), STQ1_ERR_SHAPE,
+ * STQ1_ERR_ALIGN, STQ1_ERR_CUDA.
+ */
+int stq1_selftest_product(const int8_t* xq, const float* x_scales, const int8_t* wq, const float* w_scales, float* y,
+                          int64_t T, int64_t N, int64_t K, int arrive, void* stream);
+
+/*
  * Debug build.  The library also builds as libstq1_debug.so, compiled with
  * STQ1_DEBUG.  That build bounds-checks the indices its kernels take from
  * device memory and from the call's geometry before using them:
@@ -590,6 +604,8 @@ int stq1_mix_allocate(const double* err_low, const double* err_high, const doubl
  * split are joined in a fixed order), and a row's results do not depend on what
  * the other rows hold.  Nothing but the outputs and the workspace is written.
  * Outputs and workspace must overlap neither one another nor the inputs.
+ * A product whose wait inside a kernel gives up (STQ1_DEV_WAIT_LIMIT) stores
+ * nothing of the outputs that it concerns.
  * No index is taken from device memory, so the debug build checks nothing more
  * here.  The kernel is chosen by the sizes: up to 16 tokens a streaming kernel
  * (mma.sync), else tensor-core tiles (tcgen05).

@@ -103,6 +103,8 @@ SIGNATURES = {
                                     _c.c_void_p]),
     "stq1_i8_matmul": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int,
                                   _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p]),
+    "stq1_selftest_product": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64,
+                                         _c.c_int64, _c.c_int64, _c.c_int, _c.c_void_p]),
     "stq1_i8_ffn_workspace": (_c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int64]),
     "stq1_i8_ffn": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
                                _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
@@ -636,6 +638,24 @@ def selftest_wait(arrive: bool, stream=None) -> int:
     torch = _torch()
     s = torch.cuda.current_stream() if stream is None else stream
     _check("stq1_selftest_wait", _load().stq1_selftest_wait(1 if arrive else 0, ctypes.c_void_p(s.cuda_stream)))
+    return status(s)
+
+
+def selftest_product(x_q, x_scales, w_q, w_scales, out, arrive: bool, stream=None) -> int:
+    """Runs the bounded-wait self-test of the tile kernels (see include/stq1.h) on int8 codes [T, K] and [N, K] with
+    fp32 scales, into fp32 out [T, N], and returns the device error bits."""
+    torch = _torch()
+    s = torch.cuda.current_stream() if stream is None else stream
+    (t, k), n = x_q.shape, w_q.shape[0]
+    for v, dtype, shape, name in ((x_q, torch.int8, (t, k), "x_q"), (x_scales, torch.float32, (t,), "x_scales"),
+                                  (w_q, torch.int8, (n, k), "w_q"), (w_scales, torch.float32, (n,), "w_scales"),
+                                  (out, torch.float32, (t, n), "out")):
+        _require(v, dtype, name)
+        if tuple(v.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(v.shape)}")
+    _check("stq1_selftest_product", _load().stq1_selftest_product(
+        x_q.data_ptr(), x_scales.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(), out.data_ptr(), t, n, k,
+        1 if arrive else 0, ctypes.c_void_p(s.cuda_stream)))
     return status(s)
 
 

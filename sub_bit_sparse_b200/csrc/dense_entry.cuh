@@ -131,6 +131,7 @@ struct DenseProduct {
   const float *sx, *sw;
   void* out;
   uint16_t* y;
+  int missing;                       // bytes of A per step that no copy brings (the self-test; else 0)
 };
 
 // One product on the tile kernels, or two (DUAL: d1's A is MN-major) as one launch.
@@ -147,7 +148,7 @@ DenseArgs tile_args(const DenseProduct& d, long long tiles_m, long long tiles_n,
   p.M = d.M;
   p.N = d.N;
   p.n_k = k_steps(d.K, I8);
-  p.a_bytes = a_rows * kDnStepBytes;
+  p.a_bytes = a_rows * kDnStepBytes + d.missing;
   p.tiles_m = static_cast<int>(tiles_m);
   p.tiles_n = static_cast<int>(tiles_n);
   p.sx = d.sx;
@@ -399,7 +400,7 @@ int launch_quant_i8(const void* src, int type, long long R, long long K, int8_t*
 
 DenseProduct i8_product(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, void* out, long long T,
                         long long N, long long K) {
-  return {xq, wq, T, N, K, sx, sw, out, nullptr};
+  return {xq, wq, T, N, K, sx, sw, out, nullptr, 0};
 }
 
 struct I8FfnPlan {
@@ -449,6 +450,20 @@ extern "C" int stq1_i8_matmul(const int8_t* xq, const float* x_scales, const int
   const DenseProduct p = i8_product(xq, x_scales, wq, w_scales, y, T, N, K);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return type == STQ1_TYPE_F32 ? launch_product<kEpiI8F32>(p, false, s) : launch_product<kEpiI8Bf16>(p, false, s);
+}
+
+extern "C" int stq1_selftest_product(const int8_t* xq, const float* x_scales, const int8_t* wq, const float* w_scales,
+                                     float* y, int64_t T, int64_t N, int64_t K, int arrive, void* stream) {
+  NvtxRange nvtx_range("stq1_selftest_product");
+  if (!xq || !x_scales || !wq || !w_scales || !y) return STQ1_ERR_NULL;
+  if (arrive != 0 && arrive != 1) return STQ1_ERR_ARG;
+  if (!dense_shape_ok(T, N, K) || K % 16 || K > kI8MaxK) return STQ1_ERR_SHAPE;
+  if (!aligned16(xq) || !aligned16(wq) || !aligned16(y) || (reinterpret_cast<uintptr_t>(x_scales) & 3) ||
+      (reinterpret_cast<uintptr_t>(w_scales) & 3))
+    return STQ1_ERR_ALIGN;
+  DenseProduct p = i8_product(xq, x_scales, wq, w_scales, y, T, N, K);
+  p.missing = arrive ? 0 : 16;
+  return launch_tiles<kEpiI8F32, false, false>(p, false, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int stq1_glu(const uint16_t* x, const uint16_t* W, uint16_t* act, uint16_t* y, int64_t T, int64_t N,

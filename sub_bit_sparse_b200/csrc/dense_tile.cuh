@@ -29,7 +29,7 @@ __host__ __device__ constexpr bool epi_glu(int e) { return e == kEpiI8Glu || e =
 struct DenseArgs {
   long long M, N;                    // outputs; for the gated forms N is half of B's rows
   int n_k;                           // 128-byte steps of K
-  int a_bytes;                       // bytes of A per step (split kernel)
+  int a_bytes;                       // bytes of A per step and CTA that a step waits for
   int tiles_m, tiles_n;
   const float *sx, *sw;              // int8: scales of A's rows and of B's rows
   void* out;                         // [M, N]
@@ -513,7 +513,8 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       for (int i = 0; ok && pair_unit<DUAL>(args, i, u); ++i) {
         const DenseArgs& p = args.p[u.prob];
         const int boxes = warp == kPairWarpA || u.half < 0 ? 2 : 1;
-        const uint32_t expect = rank == 0 ? boxes * kDnOperandBytes : 0;      // of both CTAs
+        // bytes of both CTAs
+        const uint32_t expect = rank != 0 ? 0 : (warp == kPairWarpA ? 2 * p.a_bytes : boxes * kDnOperandBytes);
         if (warp == kPairWarpA) {
           const int row = u.tm * 256 + static_cast<int>(rank) * kDnRows;
           if (DUAL && u.prob)
@@ -543,7 +544,8 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       PairUnit u;
       for (; ok && pair_unit<DUAL>(args, static_cast<int>(t), u); ++t) {
         const uint32_t buf = t & 1, use = t >> 1;
-        if (!dn_wait_cluster(bar_acc_empty + 8 * buf, (use & 1) ^ 1)) break;
+        ok = dn_wait_cluster(bar_acc_empty + 8 * buf, (use & 1) ^ 1);
+        if (!ok) break;
         tc_fence_after();
         const int n_k = args.p[u.prob].n_k, n = u.half < 0 ? 256 : 128;
         const uint32_t d = tmem + 256 * buf;
@@ -551,7 +553,9 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
           ok = pair_mmas<I8, true, BMN>(d, n_k, dn_idesc<I8, true, BMN>(256, n), sbase, bar_full, bar_empty, r);
         else
           ok = pair_mmas<I8, AMN, BMN>(d, n_k, dn_idesc<I8, AMN, BMN>(256, n), sbase, bar_full, bar_empty, r);
-        dn_commit_pair(bar_acc_full + 8 * buf);
+        // after a wait that ran out the sums are incomplete: the epilogue is not told of them,
+        // gives up in its turn and stores nothing of this tile
+        if (ok) dn_commit_pair(bar_acc_full + 8 * buf);
       }
       if (!ok) {
         // every MMA issued must be done before TMEM is freed (bounded)
@@ -587,7 +591,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
         for (int i = 0; i < kMine; ++i) dn_block_scales<GLU>(p, first_col(side + i * kPairSides), scale[i]);
       }
-      if (!mbar_wait_bounded(bar_acc_full + 8 * buf, use & 1)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_acc_full + 8 * buf, use & 1))) break;
       tc_fence_after();
       const uint32_t acc = lanes + 256 * buf;
       auto release = [&]() {
@@ -640,12 +644,12 @@ static_assert(kDnRows * kSplitPitch * 4 <= kSplitOffBar, "a finished piece takes
 static_assert(kSplitThreads / 32 * 12288 <= kSplitOffBar, "and so do the blocks of results");
 
 template <bool I8, bool AMN, bool BMN>
-__device__ __forceinline__ void split_mmas(uint32_t tmem, int steps, uint32_t sbase, uint32_t bar_full,
+__device__ __forceinline__ bool split_mmas(uint32_t tmem, int steps, uint32_t sbase, uint32_t bar_full,
                                            uint32_t bar_empty) {
   constexpr uint32_t idesc = dn_idesc<I8, AMN, BMN>(128, 128);
   for (int it = 0; it < steps; ++it) {
     const uint32_t s = it % kSplitStages, ph = (it / kSplitStages) & 1;
-    if (!mbar_wait_bounded(bar_full + 8 * s, ph)) break;
+    if (!mbar_wait_bounded(bar_full + 8 * s, ph)) return false;
     tc_fence_after();
     const uint64_t da = dn_desc<AMN>(sbase + s * kDnStageBytes);
     const uint64_t db = dn_desc<BMN>(sbase + s * kDnStageBytes + kDnOperandBytes);
@@ -654,6 +658,7 @@ __device__ __forceinline__ void split_mmas(uint32_t tmem, int steps, uint32_t sb
       dn_mma<I8, 1>(tmem, da + j * dn_advance<AMN>(), db + j * dn_advance<BMN>(), idesc, (it | j) != 0);
     tc_commit(bar_empty + 8 * s);
   }
+  return true;
 }
 
 struct SplitArgs {
@@ -678,7 +683,8 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
   const uint32_t sraw = smem_u32(smem_raw);
   const uint32_t sbase = (sraw + 1023u) & ~1023u;
   const uint32_t bar = sbase + kSplitOffBar;
-  const uint32_t bar_full = bar, bar_empty = bar + 64, bar_acc = bar + 128, s_tmem = bar + 144;
+  const uint32_t bar_full = bar, bar_empty = bar + 64, bar_acc = bar + 128, bar_drain = bar + 136,
+                 s_tmem = bar + 144, s_failed = bar + 148;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int piece = blockIdx.y;                      // the cluster of S runs along y
   const int prob = DUAL && static_cast<int>(blockIdx.x) >= args.tiles0 ? 1 : 0;
@@ -691,7 +697,9 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       mbar_init(bar_empty + 8 * i, 1);
     }
     mbar_init(bar_acc, 1);
+    mbar_init(bar_drain, 1);
     fence_mbar_init();
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(s_failed), "r"(0u) : "memory");
   }
   if (warp == 5) dn_tmem_alloc<1>(s_tmem, 128);
   if (warp == 4 && lane == 0) {
@@ -750,17 +758,23 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     }
   } else if (warp == 5) {
     if (lane == 0) {
-      if (DUAL && prob) split_mmas<I8, true, BMN>(tmem, k1 - k0, sbase, bar_full, bar_empty);
-      else split_mmas<I8, AMN, BMN>(tmem, k1 - k0, sbase, bar_full, bar_empty);
-      tc_commit(bar_acc);                            // all MMAs so far, in the error case too
+      bool ok;
+      if (DUAL && prob) ok = split_mmas<I8, true, BMN>(tmem, k1 - k0, sbase, bar_full, bar_empty);
+      else ok = split_mmas<I8, AMN, BMN>(tmem, k1 - k0, sbase, bar_full, bar_empty);
+      // After a wait that ran out the sums are incomplete: who waits for them is not told, gives up
+      // in its turn and stores nothing.  The MMAs issued must be done before TMEM is freed (bounded).
+      tc_commit(ok ? bar_acc : bar_drain);
+      if (!ok) mbar_wait_bounded(bar_drain, 0);
     }
   } else if (S > 1 && warp < 4) {
     // the sums to shared memory (the stages are free once the last MMA is done); an empty piece sums to zero
-    mbar_wait_bounded(bar_acc, 0);
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar_acc, 0));
     tc_fence_after();
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
     const uint32_t row = sbase + (32 * warp + lane) * (kSplitPitch * 4);
-    if (tm * static_cast<long long>(kDnRows) + 32 * warp < p.M) {
+    if (!ok) {
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(s_failed), "r"(1u) : "memory");
+    } else if (tm * static_cast<long long>(kDnRows) + 32 * warp < p.M) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t v[32];
@@ -783,7 +797,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     const float sx = I8 && row0 + lane < p.M ? p.sx[row0 + lane] : 0.f;
     float scale[2] = {};
     if constexpr (I8) dn_block_scales<GLU>(p, col0, scale);
-    if (mbar_wait_bounded(bar_acc, 0)) {
+    if (__all_sync(0xffffffffu, mbar_wait_bounded(bar_acc, 0))) {
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
       const int h = warp >> 2;
@@ -823,6 +837,9 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
       if (col < p.N) swa[i] = p.sw[(GLU && i >= 2 ? p.N : 0) + col];
     }
   }
+  // a piece without sums (lane q asks after piece q): none of the tile's rows is stored
+  uint32_t failed = 0;
+  if (lane < S) asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(failed) : "r"(dn_mapa(s_failed, lane)) : "memory");
   for (int r0 = piece + S * warp; r0 < rows; r0 += S * kWarps * kRows) {
     uint32_t w[kRows][S][4];
     float sxs[kRows];
@@ -849,6 +866,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         }
       }
     }
+    if (__any_sync(0xffffffffu, failed != 0)) break;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       if (r0 + j * S * kWarps >= rows) break;
