@@ -607,8 +607,8 @@ int stq1_mix_allocate(const double* err_low, const double* err_high, const doubl
  * A product whose wait inside a kernel gives up (STQ1_DEV_WAIT_LIMIT) stores
  * nothing of the outputs that it concerns.
  * No index is taken from device memory, so the debug build checks nothing more
- * here.  The kernel is chosen by the sizes: up to 16 tokens a streaming kernel
- * (mma.sync), else tensor-core tiles (tcgen05).
+ * here.  The kernel is chosen by the sizes: up to 16 tokens mostly a streaming
+ * kernel (mma.sync), else tensor-core tiles (tcgen05).
  */
 
 /* Element types of stq1_quantize_i8's source and stq1_i8_matmul's result. */

@@ -298,13 +298,14 @@ struct FewPlan {
 //   [4096, 7168] 5.7 -> 5.0 us), until two of the same launch come to share an SM
 //   and others stand idle, which then stays so from call to call: 12 us.
 // - more outputs than one round of CTAs, and single tiles that run at once: the
-//   tiles (int8 [16384, 4096]: 15.1 us and 14.3 on tiles at one token, 18.3 and
-//   14.6 at 16; gated [14336, 4096] at 12 tokens 26.9 and 24.8), except gated up
-//   to 8 tokens (22.3 and 24.7 at one) and where the rounds overlap because two
-//   CTAs fit an SM (int8 [11008, 4096] at one token 9.5 and 12.1).
+//   tiles (int8 [11008, 4096]: 12.7 us and 11.5 on tiles at one token, 14.4 and
+//   11.8 at 16; [18944, 4096] 16.0 and 14.9, 19.9 and 15.3; the other way for
+//   [11008, 2048], 5.7 and 6.5, and [11008, 8192], 18.5 and 19.5 at one token; gated
+//   [14336, 4096] at 12 tokens 26.0 and 24.8), except gated up to 8 tokens
+//   ([11008, 4096] 17.8 and 21.0 at one, 19.1 and 21.3 at 8).
 // - more tiles than that: int8 above 8 tokens on tiles ([65536, 2048], 12 tokens:
 //   40.1 and 36.3 us; 8 tokens: 34.6 and 36.2), the gated form here ([28672, 4096],
-//   12 tokens: 48.9 and 63.3).
+//   12 tokens: 47.9 and 64.1).
 bool plan_few(FewPlan* f, long long T, long long N, long long kbytes, bool glu, bool made = false) {
   if (T > kFewMaxTokens) return false;
   const int sms = sm_count(), unit = glu ? 8 : 16;         // the gate rows end on a whole swizzle atom
