@@ -65,7 +65,7 @@ bool few_config() {
   return few_config_one<EPI, MADE, 2, 1>() && few_config_one<EPI, MADE, 2, 2>() && few_config_one<EPI, MADE, 4, 1>() &&
          few_config_one<EPI, MADE, 4, 2>();
 }
-std::atomic<int> g_max_clusters[kMaxDevices][4];   // clusters of 1, 2, 4, 8 CTAs of the split kernel that run at once
+std::atomic<int> g_max_clusters[kMaxDevices][3];   // clusters of 2, 4, 8 CTAs of the split kernel that run at once
 template <int EPI, bool AMN, bool BMN, bool DUAL, int S>
 bool split_config() {
   return cudaFuncSetAttribute(dense_split_kernel<EPI, AMN, BMN, DUAL, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -115,10 +115,9 @@ int ensure_dense_configured() {
     cudaGetLastError();
     return STQ1_ERR_CUDA;
   }
-  g_max_clusters[dev][0].store(sm_count(), std::memory_order_relaxed);
-  g_max_clusters[dev][1].store(query_clusters<2>(), std::memory_order_relaxed);
-  g_max_clusters[dev][2].store(query_clusters<4>(), std::memory_order_relaxed);
-  g_max_clusters[dev][3].store(query_clusters<8>(), std::memory_order_relaxed);
+  g_max_clusters[dev][0].store(query_clusters<2>(), std::memory_order_relaxed);
+  g_max_clusters[dev][1].store(query_clusters<4>(), std::memory_order_relaxed);
+  g_max_clusters[dev][2].store(query_clusters<8>(), std::memory_order_relaxed);
   g_dense_configured[dev].store(true, std::memory_order_release);
   return STQ1_OK;
 }
@@ -224,7 +223,7 @@ int split_pieces(long long tiles, int n_k, int least) {
   const int dev = current_device();
   int S = 1;
   for (int i = 1; i <= 3; ++i)
-    if (dev >= 0 && tiles <= g_max_clusters[dev][i].load(std::memory_order_relaxed) && (least << i) <= n_k) S = 1 << i;
+    if (dev >= 0 && tiles <= g_max_clusters[dev][i - 1].load(std::memory_order_relaxed) && (least << i) <= n_k) S = 1 << i;
   return S;
 }
 // Joining the pieces costs about four steps whatever their number, less where

@@ -636,7 +636,6 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 
 constexpr int kSplitStages = 6;
 constexpr int kSplitThreads = 256;                  // warps 0-3 sums, 4 producer, 5 MMA; all store
-constexpr int kSplitMax = 8;                        // pieces of K: the CTAs of one cluster
 constexpr int kSplitPitch = 132;                    // words per row of a finished piece
 constexpr int kSplitOffBar = kSplitStages * kDnStageBytes;
 constexpr int kSplitSmemBytes = 1024 + kSplitOffBar + 256;
