@@ -836,7 +836,8 @@ int moe_compute(const MoePlan& m, const MoeTables& tb, const MoeScratch& sc, con
                               lut_smem_bytes(kMoeTableTokens, lut_stages(l), l.g.stage_bytes, 1), st, 1u, maps.w,
                               maps.t, l);
   };
-  if (!m.mma) return launch_lut(s);
+  // (one or two pairs in all: no expert can have enough of them for the other kernel, whose grid would be empty)
+  if (!m.mma || m.max_tiles == 0) return launch_lut(s);
   // tensor-core decode kernel: the other experts, in tiles of up to 8 pairs
   MmaArgs a{};
   a.g = geom;
