@@ -269,8 +269,8 @@ int launch_split(const DenseProduct& d0, const DenseProduct& d1, int S, bool ear
 
 // More 128 x 128 tiles than SMs: pairs on 256 x 256 tiles; else one tile per
 // CTA, K split.  At the border, int8 with [4096, 7168] weights: 512 tokens (128
-// tiles) take 18.0 us split and 20.2 on pairs, 600 tokens (160 tiles, two rounds
-// of single tiles) 24.5 us on pairs.
+// tiles) take 17.1 us split and 20.2 on pairs, 600 tokens (160 tiles, two rounds
+// of single tiles) 23.8 us on pairs.
 template <int EPI, bool AMN, bool BMN>
 int launch_tiles(const DenseProduct& d, bool early, cudaStream_t s) {
   int rc = ensure_dense_configured();
@@ -365,7 +365,7 @@ int launch_few(const FewPlan& f, const DenseProduct& d, bool early, uint32_t* am
 }
 
 // A product of K-major operands: few tokens take the streaming kernel (int8,
-// [4096, 7168]: 5.2 us at one token, 6.8 at 16; the split kernel 7.4 and 7.8).
+// [4096, 7168]: 5.2-6.4 us at one token, 6.8-7.4 at 16; the split kernel 7.4 and 7.8).
 template <int EPI>
 int launch_product(const DenseProduct& d, bool early, cudaStream_t s) {
   FewPlan f;

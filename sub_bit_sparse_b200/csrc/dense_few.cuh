@@ -11,11 +11,12 @@
 //
 // Bound by HBM and by what a launch cannot avoid, about 3 us from its start to
 // the first bytes and from the last bytes to the stored sums: int8 [4096, 7168] at
-// one token 7.1 us from HBM, 4.1 TB/s (29.4 MB alone would take 4.5), 5.2 where a
-// part of the weights is in L2, and 8.0 and 6.8 at 16; bf16 gated 10.9 us, 5.4 TB/s, 12.5 at 16.  (Loads straight
-// into registers instead of copies through shared memory: 7.7 and 14.3 us at one
-// token.)  The tokens' steps come beside the weights' as copies of their own:
-// brought whole before the first step, 16 tokens took 7.2 (L2) and 14.1.
+// one token 7.1-8.6 us from HBM, 4.1 TB/s at best (29.4 MB alone would take 4.5),
+// 5.2-6.4 where a part of the weights is in L2, and 8.0-9.3 and 6.8-7.4 at 16; bf16
+// gated 10.8 us, 5.4 TB/s, 12.3 at 16.  (Loads straight into registers instead of
+// copies through shared memory: 7.7 and 14.3 us at one token.)  The tokens' steps
+// come beside the weights' as copies of their own: brought whole before the first
+// step, 16 tokens took 7.2 (L2) and 14.1.
 //
 // A contraction may take its k in any order as long as both operands agree on
 // it.  So a lane's share of an A fragment need not be the 4-byte pieces that

@@ -630,7 +630,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 // Products with few tiles: one CTA per 128 x 128 tile and piece of K.  Bound by
 // the copies into shared memory: 32 KB per step in 436 cycles (75 bytes a clock)
 // where the MMAs take 256; below about 128 tokens by the weights' way from HBM.
-// [4096, 7168] int8: 9.1 us at 64 tokens, 10.6 at 128, 13.4 at 256, 18.0 at 512.
+// [4096, 7168] int8: 9.1 us at 64 tokens, 10.1 at 128, 12.6 at 256, 17.1 at 512.
 // (Prefetching the weights into L2 as well, from idle warps, is 5-18% slower.)
 // ---------------------------------------------------------------------------
 
